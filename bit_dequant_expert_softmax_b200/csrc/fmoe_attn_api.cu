@@ -1,0 +1,249 @@
+// C ABI of the attention layers (include/fmoe_attn.h): argument checks and launches.
+#include <atomic>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "../../include/fmoe_attn.h"
+#include "fmoe_attn_decode.cuh"
+#include "fmoe_attn_prompt.cuh"
+#include "fmoe_kv.cuh"
+
+using namespace fmoe;
+
+namespace {
+
+constexpr double kLog2e = 1.4426950408889634;
+constexpr int kMaxGridY = 65535;
+
+bool on_boundary(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+fmoe_status check_config(const fmoe_attn_config* c) {
+  if (!c || c->kv_heads < 1 || c->kv_heads > kMaxGridY || c->q_heads < c->kv_heads || c->q_heads % c->kv_heads ||
+      c->q_heads / c->kv_heads > 128 || c->head_dim < 1)
+    return FMOE_ERR_INVALID_ARG;
+  if (c->page_tokens < kKvTile || c->page_tokens > 1024 || c->page_tokens % kKvTile) return FMOE_ERR_INVALID_ARG;
+  return c->head_dim == 64 || c->head_dim == 128 ? FMOE_OK : FMOE_ERR_UNSUPPORTED;
+}
+
+// Rows of `heads` heads, `stride` elements apart.
+bool rows_ok(const void* p, int64_t stride, int heads, int D) {
+  return p && on_boundary(p, 16) && stride >= (int64_t)heads * D && stride % 8 == 0;
+}
+
+// Whether an output of T contiguous rows meets an input's memory other than as the input
+// itself, row on row.
+bool crosses(const uint16_t* in, int64_t in_stride, const uint16_t* out, int64_t T, int heads, int D) {
+  if (!in || !out || T < 1) return false;
+  const int64_t row = (int64_t)heads * D;
+  const uint16_t *in_end = in + (T - 1) * in_stride + row, *out_end = out + T * row;
+  if (out_end <= in || in_end <= out) return false;
+  return !(out == in && (in_stride == row || T == 1));
+}
+
+template <class P>
+fmoe_status launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? FMOE_OK : FMOE_ERR_CUDA;
+}
+
+// The current device's SM count (0: no device).
+int device_sms(int* device) {
+  static std::atomic<int> known[64];
+  int d = 0, n = 0;
+  if (cudaGetDevice(&d) != cudaSuccess) return 0;
+  *device = d;
+  if (d < 64 && (n = known[d].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) return 0;
+  if (d < 64) known[d].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Opts a kernel into its dynamic shared memory, once per device (`done`: a bit per device).
+template <class P>
+bool opt_in(void (*kernel)(P), size_t smem, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+struct AdWorkspace {
+  size_t ml, part, size;
+};
+AdWorkspace decode_workspace(int D) {
+  AdWorkspace w;
+  w.ml = kAdMaxBlocks * sizeof(AdRecord);
+  w.part = w.ml + (size_t)kAdMaxBlocks * 2 * 16 * 2 * sizeof(float);
+  w.size = w.part + (size_t)kAdMaxBlocks * 2 * 16 * D * sizeof(float);
+  return w;
+}
+
+template <int D, int NT>
+fmoe_status decode(AdParams& p, int sms, int device, int64_t most_units, void* stream) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t smem = AdGeom<D, NT>::kSmem;
+  if (!opt_in(attn_decode_kernel<D, NT>, smem, device, done)) return FMOE_ERR_CUDA;
+  int64_t blocks = sms * 2 < kAdMaxBlocks ? sms * 2 : kAdMaxBlocks;
+  if (blocks > most_units) blocks = most_units;
+  fmoe_status st = launch(attn_decode_kernel<D, NT>, dim3((unsigned)blocks), kAdThreads, smem, stream, p);
+  if (st != FMOE_OK) return st;
+  return launch(attn_join_kernel<D, NT>, dim3((unsigned)blocks, 8 * NT), kAjWarps * 32, 0, stream, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fmoe_kv_page_bytes(const fmoe_attn_config* c) {
+  return check_config(c) == FMOE_OK ? (size_t)kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens) : 0;
+}
+
+size_t fmoe_attn_workspace_bytes(const fmoe_attn_config* c) {
+  return check_config(c) == FMOE_OK ? decode_workspace(c->head_dim).size : 0;
+}
+
+fmoe_status fmoe_kv_append(const fmoe_attn_config* c, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                           int64_t k_stride, const uint16_t* v, int64_t v_stride, int T, const float* rope,
+                           int rope_positions, int rotary, const int32_t* positions, const int64_t* slots, void* cache,
+                           int64_t pages, uint16_t* q_out, uint16_t* k_out, uint32_t* device_error, void* stream) {
+  const fmoe_status st = check_config(c);
+  if (st != FMOE_OK) return st;
+  const int D = c->head_dim;
+  if (T < 0 || pages < 0 || rotary < 0 || rotary > D || rotary % 16) return FMOE_ERR_INVALID_ARG;
+  if (T == 0) return FMOE_OK;
+  if ((q == nullptr) != (q_out == nullptr) || (q && !rows_ok(q, q_stride, c->q_heads, D))) return FMOE_ERR_INVALID_ARG;
+  if (!rows_ok(k, k_stride, c->kv_heads, D) || !rows_ok(v, v_stride, c->kv_heads, D)) return FMOE_ERR_INVALID_ARG;
+  if (!slots || !on_boundary(slots, 8) || !cache || !on_boundary(cache, 128)) return FMOE_ERR_INVALID_ARG;
+  if (rotary && (!rope || !on_boundary(rope, 16) || !positions || !on_boundary(positions, 4) || rope_positions < 1))
+    return FMOE_ERR_INVALID_ARG;
+  if (!on_boundary(q_out, 16) || !on_boundary(k_out, 16) || !on_boundary(device_error, 4)) return FMOE_ERR_INVALID_ARG;
+  if (crosses(q, q_stride, q_out, T, c->q_heads, D) || crosses(k, k_stride, k_out, T, c->kv_heads, D))
+    return FMOE_ERR_INVALID_ARG;
+  KvAppendParams p{};
+  p.q = q, p.k = k, p.v = v;
+  p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
+  p.rope = rope, p.positions = positions, p.slots = slots;
+  p.cache = static_cast<uint8_t*>(cache);
+  p.pages = pages, p.page_bytes = kv_page_bytes(c->kv_heads, D, c->page_tokens);
+  p.q_out = q_out, p.k_out = k_out, p.err = device_error;
+  p.rope_positions = rope_positions, p.rotary = rotary;
+  p.q_heads = c->q_heads, p.kv_heads = c->kv_heads, p.page_tokens = c->page_tokens;
+  // few tokens: their heads over more blocks, one head row per lane group
+  const int per = kKvThreads / (D / 8), heads = (q ? c->q_heads : 0) + 2 * c->kv_heads;
+  int y = T < 512 ? (heads + per - 1) / per : 1;
+  if (y > kMaxGridY) y = kMaxGridY;
+  const dim3 grid((unsigned)T, (unsigned)y);
+  return D == 128 ? launch(kv_append_kernel<128>, grid, kKvThreads, 0, stream, p)
+                  : launch(kv_append_kernel<64>, grid, kKvThreads, 0, stream, p);
+}
+
+fmoe_status fmoe_kv_gather(const fmoe_attn_config* c, const void* cache, int64_t pages, const int32_t* page_table,
+                           int table_width, int seqs, const int32_t* first, const int32_t* cu, int64_t rows,
+                           uint16_t* k_out, uint16_t* v_out, uint32_t* device_error, void* stream) {
+  const fmoe_status st = check_config(c);
+  if (st != FMOE_OK) return st;
+  if (seqs < 0 || rows < 0 || rows > INT32_MAX || pages < 0 || table_width < 1) return FMOE_ERR_INVALID_ARG;
+  if (seqs == 0 || rows == 0) return FMOE_OK;
+  if (!cache || !on_boundary(cache, 128) || !page_table || !on_boundary(page_table, 4) || !cu || !on_boundary(cu, 4) ||
+      !on_boundary(first, 4) || !k_out || !on_boundary(k_out, 16) || !v_out || !on_boundary(v_out, 16) ||
+      !on_boundary(device_error, 4))
+    return FMOE_ERR_INVALID_ARG;
+  KvGatherParams p{};
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.pages = pages, p.page_bytes = kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens), p.rows = rows;
+  p.table = page_table, p.first = first, p.cu = cu;
+  p.k_out = k_out, p.v_out = v_out, p.err = device_error;
+  p.width = table_width, p.seqs = seqs, p.kv_heads = c->kv_heads, p.page_tokens = c->page_tokens;
+  const dim3 grid((unsigned)((rows + kKvGatherRows - 1) / kKvGatherRows), (unsigned)c->kv_heads);
+  return c->head_dim == 128 ? launch(kv_gather_kernel<128>, grid, kKvThreads, 0, stream, p)
+                            : launch(kv_gather_kernel<64>, grid, kKvThreads, 0, stream, p);
+}
+
+fmoe_status fmoe_attn_decode(const fmoe_attn_config* c, const uint16_t* q, int64_t q_stride, const void* cache,
+                             int64_t pages, const int32_t* page_table, int table_width, const int32_t* lens, int seqs,
+                             float scale, uint16_t* out, void* workspace, size_t workspace_bytes,
+                             uint32_t* device_error, void* stream) {
+  const fmoe_status st = check_config(c);
+  if (st != FMOE_OK) return st;
+  const int D = c->head_dim;
+  if (seqs < 0 || pages < 0 || table_width < 1 || !(scale == scale) || (int64_t)table_width * c->page_tokens > (1 << 30))
+    return FMOE_ERR_INVALID_ARG;
+  if (seqs == 0) return FMOE_OK;
+  if (!rows_ok(q, q_stride, c->q_heads, D) || !cache || !on_boundary(cache, 128) || !page_table ||
+      !on_boundary(page_table, 4) || !lens || !on_boundary(lens, 4) || !out || !on_boundary(out, 16) ||
+      !on_boundary(device_error, 4))
+    return FMOE_ERR_INVALID_ARG;
+  const AdWorkspace w = decode_workspace(D);
+  if (!workspace || workspace_bytes < w.size) return FMOE_ERR_NO_WORKSPACE;
+  if (!on_boundary(workspace, 256)) return FMOE_ERR_INVALID_ARG;
+  int device = 0;
+  const int sms = device_sms(&device);
+  if (sms == 0) return FMOE_ERR_CUDA;
+  AdParams p{};
+  p.q = q, p.q_stride = q_stride;
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.pages = pages, p.page_bytes = kv_page_bytes(c->kv_heads, D, c->page_tokens);
+  p.table = page_table, p.lens = lens, p.out = out;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.rec = reinterpret_cast<AdRecord*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.err = device_error;
+  p.scale_log2 = (float)(scale * kLog2e);
+  p.width = table_width, p.seqs = seqs, p.q_heads = c->q_heads, p.kv_heads = c->kv_heads;
+  p.group = c->q_heads / c->kv_heads, p.page_tokens = c->page_tokens;
+  // up to 8 query heads of a key/value head: one 8-column block of queries; more: two
+  const bool wide = p.group > 8;
+  p.qblocks = wide ? (p.group + 15) / 16 : 1;
+  const int64_t units =
+      (int64_t)seqs * c->kv_heads * p.qblocks * (((int64_t)table_width * c->page_tokens + kAdStep - 1) / kAdStep);
+  if (D == 128) return wide ? decode<128, 2>(p, sms, device, units, stream) : decode<128, 1>(p, sms, device, units, stream);
+  return wide ? decode<64, 2>(p, sms, device, units, stream) : decode<64, 1>(p, sms, device, units, stream);
+}
+
+fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                             int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* cu_q,
+                             const int32_t* cu_k, int seqs, int64_t q_rows, int64_t k_rows, float scale, uint16_t* out,
+                             uint32_t* device_error, void* stream) {
+  const fmoe_status st = check_config(c);
+  if (st != FMOE_OK) return st;
+  const int D = c->head_dim;
+  if (seqs < 0 || q_rows < 0 || k_rows < 0 || q_rows > INT32_MAX || k_rows > INT32_MAX || !(scale == scale))
+    return FMOE_ERR_INVALID_ARG;
+  if (seqs == 0 || q_rows == 0) return FMOE_OK;
+  if (!rows_ok(q, q_stride, c->q_heads, D) || !cu_q || !on_boundary(cu_q, 4) || !cu_k || !on_boundary(cu_k, 4) || !out ||
+      !on_boundary(out, 16) || !on_boundary(device_error, 4))
+    return FMOE_ERR_INVALID_ARG;
+  if (!rows_ok(k, k_stride, c->kv_heads, D) || !rows_ok(v, v_stride, c->kv_heads, D)) return FMOE_ERR_INVALID_ARG;
+  ApParams p{};
+  p.q = q, p.k = k, p.v = v;
+  p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride, p.q_rows = q_rows, p.k_rows = k_rows;
+  p.cu_q = cu_q, p.cu_k = cu_k, p.out = out, p.err = device_error;
+  p.scale_log2 = (float)(scale * kLog2e);
+  p.seqs = seqs, p.q_heads = c->q_heads, p.kv_heads = c->kv_heads, p.group = c->q_heads / c->kv_heads;
+  p.tile_tokens = kApRows / p.group;
+  // blocks of tile_tokens queries: at most this many over all sequences
+  const int64_t blocks = q_rows / p.tile_tokens + seqs;
+  if (blocks > INT32_MAX) return FMOE_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks, (unsigned)c->kv_heads);
+  return D == 128 ? launch(attn_prompt_kernel<128>, grid, kApThreads, 0, stream, p)
+                  : launch(attn_prompt_kernel<64>, grid, kApThreads, 0, stream, p);
+}
+
+}  // extern "C"

@@ -1,0 +1,159 @@
+/*
+ * fmoe_attn.h — C ABI of libfmoe.so for the full-attention layers beside the MoE and the
+ * GatedDeltaNet layers (the pages' model has 15 of them among its 60 layers,
+ * hotdry.top "MoE稀疏架构"): a paged key/value cache in the library's affine 4-bit format,
+ * attention of single tokens over that cache and causal attention over whole prompts.
+ *
+ * The conventions of fmoe.h hold: device pointers owned by the caller and borrowed for
+ * the call, bf16 as uint16_t bit patterns, `stream` a cudaStream_t as void* of the current
+ * device, everything asynchronous, nothing allocated, host-detectable problems returned
+ * before anything is enqueued, and no CPU fallback.
+ *
+ * Order of a serving step of one layer: project q, k, v; fmoe_kv_append; then
+ * fmoe_attn_decode (one new token per sequence) or fmoe_attn_prompt (several).
+ *
+ * device_error (every call): NULL, or a uint32_t in device memory into which the kernels
+ * OR the FMOE_DEVERR_* bits below for indices that they found out of range.  Such an index
+ * is never dereferenced: its row or its keys are left out, the rest of the call is done.
+ */
+#ifndef FMOE_ATTN_H
+#define FMOE_ATTN_H
+
+#include "fmoe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Device-side error bits of the attention entry points (beside those of fmoe.h). */
+#define FMOE_DEVERR_BAD_SLOT     0x10u /* fmoe_kv_append: slot >= pages * page_tokens            */
+#define FMOE_DEVERR_BAD_POSITION 0x20u /* fmoe_kv_append: position outside the rotation table    */
+#define FMOE_DEVERR_BAD_PAGE     0x40u /* a page table entry outside [0, pages)                  */
+#define FMOE_DEVERR_BAD_LENGTH   0x80u /* a length or row offset that is negative, decreasing or
+                                          beyond its table or tensor                             */
+
+/* Geometry of one attention layer.  q_heads is a multiple of kv_heads and at most 128 times
+ * it (query head h reads key/value head h / (q_heads / kv_heads)); head_dim (D) is 64 or
+ * 128; page_tokens (P) is a multiple of 16 up to 1024. */
+typedef struct {
+  int q_heads;
+  int kv_heads;
+  int head_dim;
+  int page_tokens;
+} fmoe_attn_config;
+
+/* ---- The cache -------------------------------------------------------------------
+ * `pages` pages of fmoe_kv_page_bytes() bytes, back to back, base 128-byte aligned.  A page
+ * holds P tokens for every key/value head: [kv_heads][P/16 tiles], a tile being 16
+ * consecutive tokens of one head:
+ *     K_Q : 16 key code rows of D/2 bytes
+ *     V_Q : 16 value code rows of D/2 bytes
+ *     K_SB: 16 rows of D/64 (scale, bias) words of the keys
+ *     V_SB: the same of the values
+ * = 16 (D + D/8) bytes: 2304 at D = 128, where a token and head take 144 bytes against 512
+ * in bf16.  Codes are 4 bits in little-endian uint32 words, 8 to a word, the lowest bits
+ * first; with n = D/64 groups, word j*n + g of a row (j = 0..7) holds channels
+ * 64g + 8j .. 64g + 8j + 7.  A (scale, bias) word holds the bf16 scale in its low half and
+ * the bf16 bias in its high half, as in the expert records: channel c of group c/64 stands
+ * for scale * code + bias.
+ *
+ * Quantisation of a group of 64 bf16 channels v (all arithmetic fp32, round to nearest
+ * even): bias = min v; scale = bf16((max/2 - min/2) / 7.5); code = rint((v/2 - min/2) /
+ * (scale/2)) limited to 0..15, 0 where scale is 0.  A group that holds an infinity or a NaN
+ * is stored as scale 0, bias NaN: it reads back as NaN throughout.
+ *
+ * Token t of a sequence lives in page page_table[t / P] at place t % P; its slot is
+ * page * P + place. */
+
+/* Bytes of one page (0 for an invalid config). */
+size_t fmoe_kv_page_bytes(const fmoe_attn_config* cfg);
+
+/* New tokens into the cache, rotated on the way.  For each of T tokens and every head,
+ * the first `rotary` (R) channels of q and k are rotated by the token's position p, channel i
+ * paired with i + R/2 (i < R/2), c = rope[p][0][i], s = rope[p][1][i]:
+ *     y_i = x_i c - x_{i+R/2} s,   y_{i+R/2} = x_{i+R/2} c + x_i s
+ * (each product and sum rounded to fp32, y to bf16); the other channels stay.  The rotated
+ * k and the v as given are quantised into slot slots[t].
+ *   q, k, v  bf16, token t's heads at q + t * q_stride (elements; heads contiguous, so
+ *            q_stride >= q_heads * D), 16-byte aligned, strides multiples of 8.  q may be
+ *            NULL (then q_out is too).
+ *   rope     fp32 [rope_positions][2][R/2] (cosines, then sines), 16-byte aligned; R is a
+ *            multiple of 16, 0 <= R <= D; ignored (with positions) when R == 0
+ *   positions int32 [T]; slots int64 [T]; slots of one call are distinct (a slot named
+ *            twice holds an unspecified mixture of the two tokens afterwards)
+ *   q_out    bf16 [T][q_heads][D], k_out bf16 [T][kv_heads][D] (may be NULL): the rotated q
+ *            and k.  q_out may be q itself (and k_out k) when its stride is that of q_out;
+ *            no other overlap of inputs and outputs is allowed.
+ * A token with a negative slot is padding: nothing of it is read or written.  A slot or
+ * position out of range sets its bit and the token is left out likewise.  T == 0 is a
+ * no-op.  Errors: INVALID_ARG, UNSUPPORTED (head_dim other than 64 and 128), CUDA. */
+fmoe_status fmoe_kv_append(const fmoe_attn_config* cfg, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                           int64_t k_stride, const uint16_t* v, int64_t v_stride, int T, const float* rope,
+                           int rope_positions, int rotary, const int32_t* positions, const int64_t* slots,
+                           void* cache, int64_t pages, uint16_t* q_out, uint16_t* k_out, uint32_t* device_error,
+                           void* stream);
+
+/* Cached tokens back as bf16(scale * code + bias), packed: for sequence s the tokens
+ * first[s] .. first[s] + cu[s+1] - cu[s] - 1 go to rows cu[s] .. cu[s+1] - 1 of k_out and
+ * v_out, bf16 [rows][kv_heads][D], 16-byte aligned (the keys and values that
+ * fmoe_attn_prompt takes where a prompt continues a cached prefix).  page_table int32
+ * [seqs][table_width]; first int32 [seqs], or NULL for zeros; cu int32 [seqs + 1],
+ * cu[0] = 0, not decreasing.  Rows from cu[seqs] on are left as they were; cu beyond `rows`
+ * sets FMOE_DEVERR_BAD_LENGTH and nothing is written past the end.  A token behind the page
+ * table's end or with a bad page sets its bit and its rows are left as they were.
+ * seqs == 0 or rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+fmoe_status fmoe_kv_gather(const fmoe_attn_config* cfg, const void* cache, int64_t pages, const int32_t* page_table,
+                           int table_width, int seqs, const int32_t* first, const int32_t* cu, int64_t rows,
+                           uint16_t* k_out, uint16_t* v_out, uint32_t* device_error, void* stream);
+
+/* ---- Single tokens over the cache --------------------------------------------------
+ * One query token per sequence, for every query head:
+ *     o = sum_j p_j v_j,  p = softmax_j(scale * q . k_j),  j < lens[s]
+ * over the cached (dequantised) keys and values, rounded once to bf16.  lens[s] <= 0 gives
+ * zeros.  q bf16 [seqs] rows q_stride elements apart (heads contiguous), 16-byte aligned,
+ * stride a multiple of 8; out bf16 [seqs][q_heads][D], 16-byte aligned; page_table int32
+ * [seqs][table_width] (entries behind a sequence's length are not read); lens int32 [seqs].
+ * A length beyond table_width * P is cut to it (and its bit set); the keys of a bad page
+ * are left out (and its bit set).  A NaN or infinity in a cached key or value reaches the
+ * outputs of its own sequence and key/value head only.
+ *
+ * workspace: fmoe_attn_workspace_bytes() bytes, 256-byte aligned, zeroed by the caller
+ * before its first use; every call leaves it ready for the next, whatever its sizes and
+ * config.  Calls (and replays of captured graphs) that share a workspace must not overlap.
+ * seqs == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, NO_WORKSPACE, CUDA. */
+fmoe_status fmoe_attn_decode(const fmoe_attn_config* cfg, const uint16_t* q, int64_t q_stride, const void* cache,
+                             int64_t pages, const int32_t* page_table, int table_width, const int32_t* lens, int seqs,
+                             float scale, uint16_t* out, void* workspace, size_t workspace_bytes,
+                             uint32_t* device_error, void* stream);
+
+/* Workspace of fmoe_attn_decode, enough for any number of sequences and any lengths (0 for an
+ * invalid config). */
+size_t fmoe_attn_workspace_bytes(const fmoe_attn_config* cfg);
+
+/* ---- Whole prompts ----------------------------------------------------------------
+ * Causal attention over packed sequences: sequence s has the queries of rows cu_q[s] ..
+ * cu_q[s+1] - 1 and the keys and values of rows cu_k[s] .. cu_k[s+1] - 1, the last query
+ * standing at the last key: with Lq queries and Lk keys, query i sees keys
+ * j <= i + Lk - Lq (all of its past and itself).  A query that sees no key gives zeros.
+ * For whole prompts cu_k is cu_q; a prompt that continues a cached prefix has the prefix's
+ * keys before its own (fmoe_kv_gather).
+ *   o_i = sum_j p_ij v_j,  p_i = softmax_j(scale * q_i . k_j), rounded once to bf16.
+ * q bf16 [q_rows], k and v bf16 [k_rows]: rows q_stride, k_stride, v_stride elements apart
+ * (heads contiguous), 16-byte aligned, strides multiples of 8; out bf16 [q_rows][q_heads][D],
+ * 16-byte aligned, not overlapping the inputs; cu_q, cu_k int32 [seqs + 1], starting at 0, not decreasing.
+ * Output rows from cu_q[seqs] on are left as they were; offsets beyond q_rows or k_rows, or
+ * decreasing ones, set FMOE_DEVERR_BAD_LENGTH and the sequences they bound are left out.
+ * Rows of other sequences and rows behind the last one never reach a sequence's outputs,
+ * whatever they hold; a NaN or infinity in a sequence's own q, k or v may reach any of its
+ * outputs of that key/value head.  page_tokens is not used.
+ * seqs == 0 or q_rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+fmoe_status fmoe_attn_prompt(const fmoe_attn_config* cfg, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                             int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* cu_q,
+                             const int32_t* cu_k, int seqs, int64_t q_rows, int64_t k_rows, float scale,
+                             uint16_t* out, uint32_t* device_error, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FMOE_ATTN_H */
