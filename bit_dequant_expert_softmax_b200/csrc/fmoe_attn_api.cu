@@ -106,6 +106,40 @@ fmoe_status decode(AdParams& p, int sms, int device, int64_t most_units, void* s
   return launch(attn_join_kernel<D, NT>, dim3((unsigned)blocks, 8 * NT), kAjWarps * 32, 0, stream, p);
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// bf16 rows of `heads` heads as {D, heads, rows}, boxes of 64 channels x box_heads x box_rows
+// (128-byte swizzled rows of 64 channels in shared memory, rows outside as zeros).
+bool row_map(CUtensorMap* m, const uint16_t* base, int D, int heads, int64_t rows, int64_t stride, int box_heads,
+             int box_rows) {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+fmoe_status prompt(const ApParams& p, void* stream) {
+  static std::atomic<uint64_t> done{0};
+  int device = 0;
+  if (device_sms(&device) == 0 || !opt_in(attn_prompt_kernel<D>, ApGeom<D>::kSmem, device, done)) return FMOE_ERR_CUDA;
+  return launch(attn_prompt_kernel<D>, dim3((unsigned)(p.units * p.kv_heads)), kApThreads, ApGeom<D>::kSmem, stream, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -231,19 +265,22 @@ fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64
       !on_boundary(out, 16) || !on_boundary(device_error, 4))
     return FMOE_ERR_INVALID_ARG;
   if (!rows_ok(k, k_stride, c->kv_heads, D) || !rows_ok(v, v_stride, c->kv_heads, D)) return FMOE_ERR_INVALID_ARG;
+  const int G = c->q_heads / c->kv_heads;
   ApParams p{};
-  p.q = q, p.k = k, p.v = v;
-  p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride, p.q_rows = q_rows, p.k_rows = k_rows;
+  p.tile_tokens = kApRows / G;
+  // units of 2 tile_tokens queries: at most this many over all sequences
+  const int64_t units = q_rows / (2 * p.tile_tokens) + seqs;
+  if (units * c->kv_heads > INT32_MAX) return FMOE_ERR_UNSUPPORTED;
+  p.units = (int)units;
+  if (!row_map(&p.tm_q, q, D, c->q_heads, q_rows, q_stride, G, p.tile_tokens) ||
+      !row_map(&p.tm_k, k, D, c->kv_heads, k_rows, k_stride, 1, kApKeys) ||
+      !row_map(&p.tm_v, v, D, c->kv_heads, k_rows, v_stride, 1, kApKeys))
+    return FMOE_ERR_CUDA;
+  p.q_rows = q_rows, p.k_rows = k_rows;
   p.cu_q = cu_q, p.cu_k = cu_k, p.out = out, p.err = device_error;
   p.scale_log2 = (float)(scale * kLog2e);
-  p.seqs = seqs, p.q_heads = c->q_heads, p.kv_heads = c->kv_heads, p.group = c->q_heads / c->kv_heads;
-  p.tile_tokens = kApRows / p.group;
-  // blocks of tile_tokens queries: at most this many over all sequences
-  const int64_t blocks = q_rows / p.tile_tokens + seqs;
-  if (blocks > INT32_MAX) return FMOE_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks, (unsigned)c->kv_heads);
-  return D == 128 ? launch(attn_prompt_kernel<128>, grid, kApThreads, 0, stream, p)
-                  : launch(attn_prompt_kernel<64>, grid, kApThreads, 0, stream, p);
+  p.seqs = seqs, p.q_heads = c->q_heads, p.kv_heads = c->kv_heads, p.group = G;
+  return D == 128 ? prompt<128>(p, stream) : prompt<64>(p, stream);
 }
 
 }  // extern "C"

@@ -1,25 +1,76 @@
 // Causal attention over packed prompts (sm_100a): o_i = softmax_j(scale q_i . k_j) v_j over the
 // keys j <= i + Lk - Lq of the query's own sequence, one pass over the keys per block of
-// query rows with the running maximum and sum of each row in registers.
+// query rows.
+//
+// Both products are GEMM-shaped and run on tcgen05 with their accumulators in tensor memory:
+//   S = Q K^T  Q and K from shared memory (TMA, 128-byte swizzle), S in tensor memory
+//   O += P V   P (bf16) from tensor memory, written over S; V from shared memory with the keys
+//              along its rows as they come (the transposed-operand form)
+// A block holds two row tiles of 128, so that one tile's softmax runs while the tensor cores
+// work on the other's products.  A row is a (token, query head of the group) pair, G heads of one
+// token in adjacent rows: a tile has 128 / G tokens of all the heads that share a key/value
+// head, which reads K and V once for the group and keeps the causal waste at 128 / G tokens.
+//
+//   warps 0-3, 4-7  softmax of row tile A, B: a thread owns a row (a tensor memory lane)
+//   warp 8          one lane issues every tcgen05.mma
+//   warp 9          one lane issues the TMA loads (warps 10, 11 fill up their warpgroup)
+// The launch gives every thread 168 registers; the softmax warps, which hold 128 scores each
+// thread, take 216 of them and the other warpgroup keeps 72 (216 * 256 + 72 * 128 = 168 * 384).
+//
+// The softmax keeps a reference r >= (running maximum - 8 in log2 units) per row: p = 2^(s - r)
+// is at most 2^8, and O, which lives in tensor memory, is rescaled only when a row's maximum
+// passes r by more than 8, which hardly ever happens after the first keys.  p is rounded to bf16
+// for the second product (V is bf16: the rounding weighs as much as V's own); its row sum is
+// taken in fp32 before the rounding.
+//
+// V rows behind the sequence's last key belong to another sequence and may hold anything: they
+// are zeroed in shared memory (0 * NaN would pass through the product).
 #pragma once
 
 #include "fmoe_attn_decode.cuh"
+#include "fmoe_tcgen05.cuh"
 
 namespace fmoe {
 
-constexpr int kApRows = 128;
-constexpr int kApKeys = 64;
-constexpr int kApThreads = 256;
+constexpr int kApRows = 128;                 // rows of a tile
+constexpr int kApKeys = 128;                 // keys of a step
+constexpr int kApThreads = 384;
+constexpr int kApMmaWarp = 8, kApLoadWarp = 9;
+constexpr unsigned long long kApWaitNs = 2000000000ull;
+constexpr float kApSlack = 8.f;              // log2 units a row's maximum may pass its reference by
 
-struct ApParams {
-  const uint16_t *q, *k, *v;
-  long long q_stride, k_stride, v_stride, q_rows, k_rows;
+struct alignas(64) ApParams {
+  CUtensorMap tm_q, tm_k, tm_v;  // {D, heads, rows}; boxes of 64 channels x G heads x tile_tokens, x 1 x 128
+  long long q_rows, k_rows;
   const int32_t *cu_q, *cu_k;
   uint16_t* out;
   uint32_t* err;
-  float scale_log2;
-  int seqs, q_heads, kv_heads, group, tile_tokens;
+  float scale_log2;  // scale * log2(e)
+  int seqs, q_heads, kv_heads, group, tile_tokens, units;
 };
+
+template <int D>
+struct ApGeom {
+  static constexpr int kHalves = D / 64;               // 128-byte wide column blocks
+  static constexpr int kBlock = 128 * 128;             // 128 rows of 128 bytes
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kQ = 0;                         // [2 tiles][halves]
+  static constexpr int kK = kQ + 2 * kHalves * kBlock; // [stages][halves]
+  static constexpr int kV = kK + kStages * kHalves * kBlock;
+  static constexpr int kBars = kV + kStages * kHalves * kBlock;
+  static constexpr int kSmem = kBars + 512 + 1024;     // + alignment
+  static constexpr uint32_t kTmemS = 0, kTmemO = 256;  // columns: S of tile x at 128 x, O at 256 + D x
+};
+
+struct ApBars {
+  uint64_t q_full[2];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t drain;
+  int abort_flag;
+  uint32_t tmem;
+};
+static_assert(sizeof(ApBars) <= 512, "barrier block");
 
 // The sequence and first query of row block `tile` of the packed sequences' line of blocks;
 // false behind the last one.  Every warp finds it for itself.
@@ -37,7 +88,7 @@ __device__ __forceinline__ bool ap_span(const int32_t* cu, int s, long long rows
   }
   return true;
 }
-__device__ __forceinline__ bool ap_find(const ApParams& p, long long tile, ApTile& r) {
+__device__ __forceinline__ bool ap_find(const ApParams& p, long long tile, int tile_tokens, ApTile& r) {
   const int lane = threadIdx.x & 31;
   long long base = 0;
   for (int s0 = 0; s0 < p.seqs; s0 += 32) {
@@ -49,7 +100,7 @@ __device__ __forceinline__ bool ap_find(const ApParams& p, long long tile, ApTil
         kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
       }
     }
-    const int mine = (nq + p.tile_tokens - 1) / p.tile_tokens;
+    const int mine = (nq + tile_tokens - 1) / tile_tokens;
     long long upto = mine;
 #pragma unroll
     for (int x = 1; x < 32; x *= 2) {
@@ -63,7 +114,7 @@ __device__ __forceinline__ bool ap_find(const ApParams& p, long long tile, ApTil
       r.nq = __shfl_sync(0xffffffffu, nq, who);
       r.k0 = __shfl_sync(0xffffffffu, k0, who);
       r.nk = __shfl_sync(0xffffffffu, nk, who);
-      r.first = static_cast<int>(tile - (base + __shfl_sync(0xffffffffu, upto - mine, who))) * p.tile_tokens;
+      r.first = static_cast<int>(tile - (base + __shfl_sync(0xffffffffu, upto - mine, who))) * tile_tokens;
       return true;
     }
     base += __shfl_sync(0xffffffffu, upto, 31);
@@ -71,131 +122,335 @@ __device__ __forceinline__ bool ap_find(const ApParams& p, long long tile, ApTil
   return false;
 }
 
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+// Shared-memory descriptors of 128-byte swizzled operands (1024-byte aligned blocks of 128-byte
+// rows).  K-major: 8-row groups 1024 bytes apart (the other offset is not used).  Transposed (the
+// 64 columns of a row are the M/N extent): 8-row groups of K 1024 bytes apart, 64-column blocks
+// `lbo` bytes apart.
+__device__ __forceinline__ uint64_t ap_desc(uint32_t saddr, uint32_t lbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+// bf16 x bf16 -> f32, M = 128, N = n, B transposed or not
+__device__ __forceinline__ uint32_t ap_idesc(int n, bool b_trans) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_trans ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr)
+      : "memory");
 }
 
-// A block takes 128 rows of one key/value head, row = token * G + query head of the group
-// (tile_tokens = 128 / G tokens), a warp 16 of them; the keys go by 64.
+// Behind the wait for a load: no use of its registers is moved before it.
+__device__ __forceinline__ void tmem_landed32(float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile("" : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                    "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]));
+  asm volatile("" : "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]),
+                    "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]), "+r"(u[30]), "+r"(u[31]));
+}
+
 template <int D>
-__global__ void __launch_bounds__(kApThreads) attn_prompt_kernel(const __grid_constant__ ApParams p) {
-  constexpr int kPitch = D + 8;
-  __shared__ __align__(16) uint16_t sk[kApKeys][kPitch], sv[kApKeys][kPitch];
-  grid_launch_dependents();
-  grid_dependency_wait();
+struct ApBlock {
+  using Gm = ApGeom<D>;
+  const ApParams& p;
+  uint8_t* base;
+  ApBars* bar;
   ApTile T;
-  if (!ap_find(p, blockIdx.x, T)) return;
-  const int kvh = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // rows g and g + 8 of the warp's 16
-  int tok[2], head[2];
-  bool live[2];
-  int sees[2];
-  uint32_t qf[D / 16][4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = warp * 16 + g + 8 * h;
-    tok[h] = T.first + row / p.group;
-    head[h] = kvh * p.group + row % p.group;
-    live[h] = row < p.tile_tokens * p.group && tok[h] < T.nq;
-    sees[h] = live[h] ? tok[h] + T.nk - T.nq + 1 : 0;  // keys [0, sees)
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (T.q0 + tok[h]) * p.q_stride + static_cast<long long>(head[h]) * D);
+  int kvh;
+  int steps[2];  // key steps of the two row tiles
+
+  __device__ __forceinline__ uint8_t* q_at(int x) const { return base + Gm::kQ + x * Gm::kHalves * Gm::kBlock; }
+  __device__ __forceinline__ uint8_t* k_at(int s) const { return base + Gm::kK + s * Gm::kHalves * Gm::kBlock; }
+  __device__ __forceinline__ uint8_t* v_at(int s) const { return base + Gm::kV + s * Gm::kHalves * Gm::kBlock; }
+
+  // A bounded wait: false once the time is up or (unless it is for the end of work in
+  // flight) another role has given up.
+  __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, bool drain = false) const {
+    if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_sleep(b, parity, 100000u)) {
+      if (!drain && *reinterpret_cast<volatile const int*>(&bar->abort_flag)) return false;
+      if (global_timer_ns() - t0 > kApWaitNs) {
+        *reinterpret_cast<volatile int*>(&bar->abort_flag) = 1;
+        kv_error(p.err, FMOE_DEVERR_COPY_TIMEOUT);
+        return false;
+      }
+    }
+    return true;
+  }
+
+  // ---- loads: one lane
+  __device__ void load() {
+    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * 128u;
+    for (int x = 0; x < 2; ++x) {
+      if (steps[x] == 0) continue;
+      mbar_arrive_expect_tx(&bar->q_full[x], q_bytes * Gm::kHalves);
+      for (int h = 0; h < Gm::kHalves; ++h)
+        tma_load_3d(q_at(x) + h * Gm::kBlock, &p.tm_q, &bar->q_full[x], 64 * h, kvh * p.group, T.q0 + T.first + x * p.tile_tokens);
+      if (x == 0) load_kv(0, true);
+    }
+    const int n = max(steps[0], steps[1]);
+    if (steps[0] == 0) load_kv(0, true);
+    int k = 1, v = 0;  // loads issued
+    while (v < n && load_kv(v, false)) {
+      if (++v == n || !load_kv(k, true)) break;
+      ++k;
+    }
+    // copies still in flight land before the block ends
+    for (int x = 0; x < 2; ++x)
+      if (steps[x] > 0) wait(&bar->q_full[x], 0, true);
+    for (int i = max(0, k - Gm::kStages); i < k; ++i) wait(&bar->k_full[i % Gm::kStages], (i / Gm::kStages) & 1, true);
+    for (int i = max(0, v - Gm::kStages); i < v; ++i) wait(&bar->v_full[i % Gm::kStages], (i / Gm::kStages) & 1, true);
+  }
+  __device__ __forceinline__ bool load_kv(int j, bool key) {
+    const int s = j % Gm::kStages, use = j / Gm::kStages;
+    uint64_t* full = key ? &bar->k_full[s] : &bar->v_full[s];
+    if (use > 0 && !wait(key ? &bar->k_empty[s] : &bar->v_empty[s], (use - 1) & 1)) return false;
+    mbar_arrive_expect_tx(full, Gm::kHalves * Gm::kBlock);
+    for (int h = 0; h < Gm::kHalves; ++h)
+      tma_load_3d((key ? k_at(s) : v_at(s)) + h * Gm::kBlock, key ? &p.tm_k : &p.tm_v, full, 64 * h, kvh, T.k0 + j * kApKeys);
+    return true;
+  }
+
+  // ---- products: one lane.  Products of one thread run in the order of their issue, so
+  // S(j + 1) may be issued behind the product that reads P(j) from the same columns.
+  __device__ __forceinline__ bool score(int x, int j, uint32_t tmem) {
+    const int s = j % Gm::kStages;
+    if (!wait(&bar->k_full[s], (j / Gm::kStages) & 1)) return false;
+    tc_fence_after();
+    const uint32_t idesc = ap_idesc(kApKeys, false);
+    const uint64_t a = ap_desc(smem_u32(q_at(x)), 16), b = ap_desc(smem_u32(k_at(s)), 16);
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
-      qf[c][h] = live[h] ? __ldg(src + 8 * c + t) : 0u;
-      qf[c][h + 2] = live[h] ? __ldg(src + 8 * c + t + 4) : 0u;
+      const uint64_t at = (static_cast<uint64_t>(c / 4) * Gm::kBlock + (c % 4) * 32) >> 4;
+      umma_ss(tmem + Gm::kTmemS + 128 * x, a + at, b + at, idesc, c > 0);
     }
+    umma_commit(&bar->s_full[x]);
+    return true;
   }
-  const int last = min(T.nq, T.first + p.tile_tokens) - 1;
-  const int keys = max(0, min(T.nk, last + T.nk - T.nq + 1));
-  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  __device__ __forceinline__ bool value(int x, int j, uint32_t tmem) {
+    const int s = j % Gm::kStages;
+    if (!wait(&bar->p_full[x], j & 1) || !wait(&bar->v_full[s], (j / Gm::kStages) & 1)) return false;
+    tc_fence_after();
+    const uint32_t idesc = ap_idesc(D, true);
+    const uint64_t b = ap_desc(smem_u32(v_at(s)), Gm::kBlock);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  for (int j0 = 0; j0 < keys; j0 += kApKeys) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kApKeys * (D / 8); i += kApThreads) {
-      const int r = i / (D / 8), c = i % (D / 8) * 8;
-      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-      if (j0 + r < keys) {
-        a = __ldg(reinterpret_cast<const uint4*>(p.k + (T.k0 + j0 + r) * p.k_stride + static_cast<long long>(kvh) * D + c));
-        b = __ldg(reinterpret_cast<const uint4*>(p.v + (T.k0 + j0 + r) * p.v_stride + static_cast<long long>(kvh) * D + c));
+    for (int c = 0; c < kApKeys / 16; ++c)
+      umma_ts(tmem + Gm::kTmemO + D * x, tmem + Gm::kTmemS + 128 * x + 8 * c, b + ((c * 2048) >> 4), idesc, j > 0 || c > 0);
+    umma_commit(&bar->o_full[x]);
+    return true;
+  }
+  __device__ void multiply(uint32_t tmem) {
+    const int n = max(steps[0], steps[1]);
+    bool ok = true;
+    for (int x = 0; x < 2 && ok; ++x)
+      if (steps[x] > 0) ok = wait(&bar->q_full[x], 0) && score(x, 0, tmem);
+    if (ok) umma_commit(&bar->k_empty[0]);
+    for (int j = 0; j < n && ok; ++j) {
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (j < steps[x]) ok = value(x, j, tmem);
+        if (ok && j + 1 < steps[x]) ok = score(x, j + 1, tmem);
       }
-      *reinterpret_cast<uint4*>(&sk[r][c]) = a;
-      *reinterpret_cast<uint4*>(&sv[r][c]) = b;
+      if (!ok) break;
+      umma_commit(&bar->v_empty[j % Gm::kStages]);
+      if (j + 1 < n) umma_commit(&bar->k_empty[(j + 1) % Gm::kStages]);
     }
-    __syncthreads();
-    float s[kApKeys / 8][4];
+    umma_commit(&bar->drain);  // nothing reads or writes tensor memory after this
+    wait(&bar->drain, 0, true);
+  }
+
+  // ---- softmax of row tile x: thread = row
+  __device__ void soften(int x, uint32_t tmem) {
+    const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
+    const uint32_t ts = tmem + lanes + Gm::kTmemS + 128 * x, to = tmem + lanes + Gm::kTmemO + D * x;
+    const int tok = T.first + x * p.tile_tokens + row / p.group, head = kvh * p.group + row % p.group;
+    const bool live = row < p.tile_tokens * p.group && tok < T.nq;
+    const int sees = live ? tok + T.nk - T.nq + 1 : 0;
+    // (a scale of zero as one that changes no weight: a key left out stays at minus infinity)
+    const float c = fmaxf(fabsf(p.scale_log2), 1e-37f), slack = kApSlack / c;
+    float ref = -INFINITY, l = 0.f;
+    for (int j = 0; j < steps[x]; ++j) {
+      if (!__all_sync(0xffffffffu, wait(&bar->s_full[x], j & 1))) return;
+      tc_fence_after();
+      float s[kApKeys];
 #pragma unroll
-    for (int i = 0; i < kApKeys / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      for (int i = 0; i < kApKeys; i += 32) tmem_ld32(ts + i, s + i);
+      tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c)
+      for (int i = 0; i < kApKeys; i += 32) tmem_landed32(s + i);
+      if (p.scale_log2 < 0.f) {
 #pragma unroll
-      for (int i = 0; i < kApKeys / 16; ++i) {
-        uint32_t b[4];
-        ldmatrix4(b, smem_u32(&sk[16 * i + (lane & 7) + (lane >> 4) * 8][16 * c + ((lane >> 3) & 1) * 8]));
-        mma_bf16(s[2 * i], qf[c][0], qf[c][1], qf[c][2], qf[c][3], b[0], b[1]);
-        mma_bf16(s[2 * i + 1], qf[c][0], qf[c][1], qf[c][2], qf[c][3], b[2], b[3]);
+        for (int i = 0; i < kApKeys; ++i) s[i] = -s[i];
       }
+      const int lim = sees - j * kApKeys;
+      if (__any_sync(0xffffffffu, lim < kApKeys)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mx = -INFINITY;
+        for (int i = 0; i < kApKeys; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int i = 0; i < kApKeys / 8; ++i)
+      for (int i = 4; i < kApKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool far = ref == -INFINITY ? top > -INFINITY : top - ref > slack;
+      if (__any_sync(0xffffffffu, far)) {
+        const float now = far ? top : ref;
+        if (j > 0) {
+          const float f = now == ref ? 1.f : ref == -INFINITY ? 0.f : ex2((ref - now) * c);
+          l *= f;
+          // the products up to step j - 1 are in O
+          if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (j - 1) & 1))) return;
+          tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& x = s[i][2 * h + e];
-          x = j0 + 8 * i + 2 * t + e < sees[h] ? x * p.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, x);
+          for (int i = 0; i < D; i += 32) {
+            float o[32];
+            tmem_ld32(to + i, o);
+            tmem_wait_ld();
+            tmem_landed32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
+            tmem_st32(to + i, w);
+          }
         }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float now = fmaxf(m[h], mx), ref = now == -INFINITY ? 0.f : now, al = ex2(m[h] - ref);
-      m[h] = now;
-      l[h] *= al;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][2 * h] *= al;
-        o[i][2 * h + 1] *= al;
+        ref = now;
       }
+      const float off = ref == -INFINITY ? 0.f : -ref * c;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < kApKeys / 8; ++i)
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& x = s[i][2 * h + e];
-          x = ex2(x - ref);
-          l[h] += x;
+        for (int i = 0; i < 32; ++i) {
+          const float a = ex2(fmaf(s[64 * h + 2 * i], c, off)), b = ex2(fmaf(s[64 * h + 2 * i + 1], c, off));
+          sum[2 * (i & 1)] += a;
+          sum[2 * (i & 1) + 1] += b;
+          w[i] = pack_bf16(a, b);
         }
+        tmem_st32(ts + 32 * h, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if ((j + 1) * kApKeys > T.nk) {  // the sequence's last, partial step: V behind it as zeros
+        if (!__all_sync(0xffffffffu, wait(&bar->v_full[j % Gm::kStages], (j / Gm::kStages) & 1))) return;
+        const int first = T.nk - j * kApKeys;
+        for (int i = threadIdx.x & 127; i < (kApKeys - first) * Gm::kHalves * 8; i += 128) {
+          const int r = first + i / (8 * Gm::kHalves), e = i % (8 * Gm::kHalves);
+          *reinterpret_cast<uint4*>(v_at(j % Gm::kStages) + (e / 8) * Gm::kBlock + r * 128 + (e % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->p_full[x]);
+    }
+    // the output rows (zeros where a row has seen nothing)
+    uint16_t* dst = p.out + ((static_cast<long long>(T.q0) + tok) * p.q_heads + head) * D;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (steps[x] > 0) {
+      if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (steps[x] - 1) & 1))) return;
+      tc_fence_after();
     }
 #pragma unroll
-    for (int c = 0; c < kApKeys / 16; ++c) {
-      const uint32_t a0 = pack_bf16(s[2 * c][0], s[2 * c][1]), a1 = pack_bf16(s[2 * c][2], s[2 * c][3]);
-      const uint32_t a2 = pack_bf16(s[2 * c + 1][0], s[2 * c + 1][1]), a3 = pack_bf16(s[2 * c + 1][2], s[2 * c + 1][3]);
+    for (int i = 0; i < D; i += 32) {
+      float o[32];
+      if (steps[x] > 0) {
+        tmem_ld32(to + i, o);
+        tmem_wait_ld();
+        tmem_landed32(o);
+      } else {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t b[4];
-        ldmatrix4_trans(b, smem_u32(&sv[16 * c + (lane & 15)][16 * i + (lane >> 4) * 8]));
-        mma_bf16(o[2 * i], a0, a1, a2, a3, b[0], b[1]);
-        mma_bf16(o[2 * i + 1], a0, a1, a2, a3, b[2], b[3]);
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      }
+      if (live) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4*>(dst + i + e) =
+              make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                         pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
       }
     }
+    tc_fence_before();
   }
+};
+
+// Blocks over (unit, key/value head), heads fastest and a sequence's last queries, which see
+// the most keys, first.
+template <int D>
+__global__ void __launch_bounds__(kApThreads, 1) attn_prompt_kernel(const __grid_constant__ ApParams p) {
+  using Gm = ApGeom<D>;
+  extern __shared__ uint8_t ap_smem[];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  uint8_t* base = ap_smem + ((1024u - (smem_u32(ap_smem) & 1023u)) & 1023u);
+  ApBlock<D> B{p, base, reinterpret_cast<ApBars*>(base + Gm::kBars)};
+  if (!ap_find(p, p.units - 1 - static_cast<int>(blockIdx.x / p.kv_heads), 2 * p.tile_tokens, B.T)) return;
+  B.kvh = blockIdx.x % p.kv_heads;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    if (!live[h]) continue;
-    const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((T.q0 + tok[h]) * static_cast<long long>(p.q_heads) + head[h]) * D);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) dst[4 * i + t] = pack_bf16(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
+  for (int x = 0; x < 2; ++x) {
+    const int t0 = B.T.first + x * p.tile_tokens, last = min(B.T.nq, t0 + p.tile_tokens) - 1;
+    const int keys = t0 < B.T.nq ? max(0, last + B.T.nk - B.T.nq + 1) : 0;
+    B.steps[x] = (keys + kApKeys - 1) / kApKeys;
   }
+  ApBars* bar = B.bar;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->q_full[i], 1);
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->p_full[i], 4);
+      mbar_init(&bar->o_full[i], 1);
+    }
+    for (int i = 0; i < Gm::kStages; ++i) {
+      mbar_init(&bar->k_full[i], 1);
+      mbar_init(&bar->k_empty[i], 1);
+      mbar_init(&bar->v_full[i], 1);
+      mbar_init(&bar->v_empty[i], 1);
+    }
+    mbar_init(&bar->drain, 1);
+    bar->abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kApMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar->tmem)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    B.soften(warp >> 2, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (max(B.steps[0], B.steps[1]) > 0 && lane == 0) {
+      if (warp == kApMmaWarp) B.multiply(tmem);
+      if (warp == kApLoadWarp) B.load();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kApMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 }  // namespace fmoe
