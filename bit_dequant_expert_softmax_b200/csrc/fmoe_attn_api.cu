@@ -95,12 +95,13 @@ AdWorkspace decode_workspace(int D) {
 }
 
 template <int D, int NT>
-fmoe_status decode(AdParams& p, int sms, int device, int64_t most_units, void* stream) {
+fmoe_status decode(AdParams& p, int sms, int device, int64_t places, void* stream) {
   static std::atomic<uint64_t> done{0};
   constexpr size_t smem = AdGeom<D, NT>::kSmem;
   if (!opt_in(attn_decode_kernel<D, NT>, smem, device, done)) return FMOE_ERR_CUDA;
-  int64_t blocks = sms * 2 < kAdMaxBlocks ? sms * 2 : kAdMaxBlocks;
-  if (blocks > most_units) blocks = most_units;
+  int64_t blocks = sms * AdGeom<D, NT>::kBlocks;
+  if (blocks > kAdMaxBlocks) blocks = kAdMaxBlocks;
+  if (blocks * kAdWarps > places) blocks = (places + kAdWarps - 1) / kAdWarps;  // a warp takes one place at least
   fmoe_status st = launch(attn_decode_kernel<D, NT>, dim3((unsigned)blocks), kAdThreads, smem, stream, p);
   if (st != FMOE_OK) return st;
   return launch(attn_join_kernel<D, NT>, dim3((unsigned)blocks, 8 * NT), kAjWarps * 32, 0, stream, p);
@@ -240,15 +241,18 @@ fmoe_status fmoe_attn_decode(const fmoe_attn_config* c, const uint16_t* q, int64
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.err = device_error;
   p.scale_log2 = (float)(scale * kLog2e);
+  p.scale_up = p.scale_log2 * kAdDown;
+  p.page_tiles = c->page_tokens / kKvTile;
+  p.tiles_magic = ((1ull << 32) + p.page_tiles - 1) / p.page_tiles;  // exact below 2^26 tiles (page_tiles <= 64)
   p.width = table_width, p.seqs = seqs, p.q_heads = c->q_heads, p.kv_heads = c->kv_heads;
   p.group = c->q_heads / c->kv_heads, p.page_tokens = c->page_tokens;
   // up to 8 query heads of a key/value head: one 8-column block of queries; more: two
   const bool wide = p.group > 8;
   p.qblocks = wide ? (p.group + 15) / 16 : 1;
-  const int64_t units =
-      (int64_t)seqs * c->kv_heads * p.qblocks * (((int64_t)table_width * c->page_tokens + kAdStep - 1) / kAdStep);
-  if (D == 128) return wide ? decode<128, 2>(p, sms, device, units, stream) : decode<128, 1>(p, sms, device, units, stream);
-  return wide ? decode<64, 2>(p, sms, device, units, stream) : decode<64, 1>(p, sms, device, units, stream);
+  const int64_t places =
+      (int64_t)seqs * c->kv_heads * p.qblocks * ((int64_t)table_width * p.page_tiles + kAdPairCost);
+  if (D == 128) return wide ? decode<128, 2>(p, sms, device, places, stream) : decode<128, 1>(p, sms, device, places, stream);
+  return wide ? decode<64, 2>(p, sms, device, places, stream) : decode<64, 1>(p, sms, device, places, stream);
 }
 
 fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64_t q_stride, const uint16_t* k,

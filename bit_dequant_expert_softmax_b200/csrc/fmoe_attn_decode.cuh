@@ -10,22 +10,28 @@
 // m16n8k16 with the cache as the 16-row operand and 8 queries as the columns: one query
 // token has at most G rows of work per key, and the tcgen05 forms (64 or 128 rows from shared
 // or tensor memory) would need every dequantised operand written to memory again.
-//   codes    enter as the exact bf16 1 + c/16 (one rotate and one LOP3 per pair)
-//   scores   per group D = sum_c (1 + c/16) q_c, X = sum_c q_c:  sum_c k_c q_c = 16 a D + (b - 16 a) X
+//   codes    enter as bf16 without conversion: a code masked in place in the low byte of a half
+//            word reads as c 2^-133 (low nibble) or c 2^-129 (high nibble), subnormal or in the
+//            first normal binade, both exact operands of the product; the other operand carries
+//            2^60 (2^56) against it, so sums sit near 2^-73.  Five instructions make the four
+//            pairs of a word (one shift, four masks).
+//   scores   per group D = sum_c c q_c, X = sum_c q_c:  sum_c k_c q_c = a D + b X
 //   values   the weights enter as p' = bf16(p a), per group.  With c - 8 as the code's centre
-//            p (a c + b) = p' (c - 8) + p (b + 8 a), and sum p' (c - 8) = 16 sum p' (1 + c/16) -
-//            24 sum p': only the centred part carries p' 's rounding, so it weighs no more than
-//            rounding p does with bf16 values.  Sums, maxima and the b part are fp32.
+//            p (a c + b) = p' (c - 8) + p (b + 8 a): only the centred part carries p' 's rounding,
+//            so it weighs no more than rounding p does with bf16 values.  The -8 sum p' comes from
+//            one more product with a constant row operand.  Sums, maxima and the b part are fp32.
 // A warp's scores leave the first product with keys in rows; movmatrix turns 8x8 blocks of
 // the packed weights into the second product's column operand.
 //
-// Split: the (sequence, key/value head, query block, 64-key step) units of the batch form one
-// line that is cut into equal ranges, one per block, found from the lengths on the device (so a
-// captured graph follows growing lengths).  A block's part of one sequence and head is a
-// segment; its tiles of 16 keys go to the warps in equal runs.  Each warp streams its tiles
-// through its own ring of bulk copies, with its own running maximum; warps join in shared
-// memory at the segment's end.  A segment that is a whole (sequence, head) is written to the
-// output, other segments to the workspace, where a second kernel joins them.
+// Split: the tiles of 16 keys of all (sequence, key/value head, query block) pairs form one line
+// that is cut into equal ranges, one per warp, found from the lengths on the device (so a
+// captured graph follows growing lengths).  A pair counts kAdPairCost tiles more than it has, for
+// its queries and its end.  A warp streams its tiles through its own ring of bulk copies and
+// keeps its own sums; nothing waits for another warp until the block's end, where the parts of
+// pairs that lie in several of its warps are joined in shared memory.  A pair that lies in one
+// block goes to the output, parts of others to the workspace, where a second kernel joins them.
+// Per query the exponentials refer to a value at most 2^8 below the running maximum, so that
+// the sums are rescaled a few times per pair and not at every new maximum.
 #pragma once
 
 #include "fmoe_kv.cuh"
@@ -34,14 +40,16 @@ namespace fmoe {
 
 constexpr int kAdWarps = 4;
 constexpr int kAdThreads = kAdWarps * 32;
-constexpr int kAdStepTiles = 4;                        // tiles a warp takes at once
-constexpr int kAdStep = kAdStepTiles * kKvTile;        // keys of a unit
-constexpr int kAdStages = 2;                           // ring slots per warp
-constexpr int kAdMaxBlocks = 512;
+constexpr int kAdPairCost = 3;                         // tiles' worth of a pair's start and end
+constexpr float kAdSlack = 8.f;                        // log2 units a maximum may pass the reference by
+constexpr float kAdUp = 0x1p60f, kAdUpHigh = 0x1p56f;  // against codes in low and high nibbles
+constexpr float kAdDown = 0x1p73f;                     // 2^133 / 2^60
+constexpr float kAdLog = 60.f;                         // the weights' 2^60, in the exponent
+constexpr int kAdMaxBlocks = 640;
 constexpr unsigned long long kAdWaitNs = 2000000000ull;
 
-// What a block leaves for the joining kernel: it ended a segment that began in block
-// `first` (-1: none).
+// What a block leaves for the joining kernel: it ended a pair that began in block `first`
+// (-1: none).
 struct AdRecord {
   int first, seq, head0, queries;
 };
@@ -57,8 +65,9 @@ struct AdParams {
   float* part;      // [blocks][2][queries][D]
   float* part_ml;   // [blocks][2][queries][2]
   uint32_t* err;
-  float scale_log2; // scale * log2(e)
-  int width, seqs, q_heads, kv_heads, group, qblocks, page_tokens;
+  float scale_log2, scale_up;  // scale * log2(e); the same times 2^73
+  unsigned long long tiles_magic;  // ceil(2^32 / page_tiles)
+  int page_tiles, width, seqs, q_heads, kv_heads, group, qblocks, page_tokens;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -78,9 +87,16 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// codes i and i + 4 of a word as bf16 1 + c/16
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
-  return (__funnelshift_r(w, w, (4 * i - 3) & 31) & 0x00780078u) | 0x3F803F80u;
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Codes i and i + 4 of a word (w8 = w >> 8): c 2^-133 for even i, c 2^-129 for odd i.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w8, int i) {
+  return (i < 2 ? w : w8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
 
 __device__ __forceinline__ int ad_len(const AdParams& p, int s) {
@@ -89,22 +105,50 @@ __device__ __forceinline__ int ad_len(const AdParams& p, int s) {
   return len <= 0 ? 0 : len > most ? static_cast<int>(most) : len;
 }
 
+#ifndef AD_T
+#define AD_T 3
+#define AD_S 2
+#define AD_B 3
+#endif
 template <int D, int NT>
 struct AdGeom {
+  static constexpr int kTake = NT == 1 ? AD_T : 2;    // tiles a warp takes at once
+  static constexpr int kStages = NT == 1 ? AD_S : 3;  // ring slots per warp
+  static constexpr int kBlocks = NT == 1 ? AD_B : 2;  // blocks per SM
   static constexpr int kTile = KvGeom<D>::kTileBytes;
-  static constexpr int kStage = kAdStepTiles * kTile;
+  static constexpr int kStage = kTake * kTile;
   static constexpr int kRegs = 16 * KvGeom<D>::kGroups * NT;  // output floats of a thread
-  static constexpr int kMerge = 32 * (kRegs + 4 * NT) * 4;    // a warp's state, bytes
-  static constexpr int kRing = kAdWarps * kAdStages * kStage;
-  static constexpr int kSmem = kRing + kAdWarps / 2 * kMerge + kAdWarps * kAdStages * 8;
+  static constexpr int kState = 32 * (kRegs + 4 * NT) * 4;    // a warp's sums, bytes
+  static constexpr int kRing = kStages * kStage;              // of a warp
+  static constexpr int kWarp = kRing + kState;                // its ring and the part it began with
+  static constexpr int kInfo = kAdWarps * kWarp;
+  static constexpr int kBars = kInfo + kAdWarps * 32;
+  static constexpr int kSmem = kBars + kAdWarps * kStages * 8;
+  static_assert(kState <= kRing, "the part that a warp ends with goes into its ring");
 };
 
-// One place in the block's line of units, the same in all of its warps.
+// A warp's parts of pairs that it shares with other warps.
+struct AdInfo {
+  int some;            // it had tiles
+  int head, head_ends; // it began within a pair; and saw that pair's end
+  int tail;            // it ended within a pair that it began
+  int seq, hb;         // the pair of `head`
+  long long pair_x;    // its place in the line
+};
+static_assert(sizeof(AdInfo) == 32, "space set aside");
+
+// A warp's way along the line.
 struct AdCursor {
-  long long left;    // units of the block not yet in a segment
-  int seq, hb;       // the next segment's sequence and (head, query block)
-  int step;          // its first 64-key step
-  int len, steps;    // of `seq`
+  long long x, end;    // what is left of its range
+  long long pair_x;    // the current pair: its first place,
+  int seq, hb;         // sequence and (head, query block),
+  int len, tiles;      // length and tiles
+};
+
+// Tiles [a, b) of a pair.
+struct AdPart {
+  int seq, hb, kvh, len, tiles, a, b;
+  long long pair_x;
 };
 
 template <int D, int NT>
@@ -116,66 +160,78 @@ struct AdWarp {
   const int warp, lane, g, t;
   const int hbs;               // (head, query block) pairs per sequence
   uint8_t* ring;
+  float* head;                 // the part of the pair that the warp began within
+  AdInfo* info;                // of all the block's warps
   uint64_t* bars;
-  float* merge;
   bool lost = false;           // a copy's wait ran out
+  int page0 = 0, pages = 0;    // page table entries page0 .. of the pair being fetched, one per lane
 
   // online softmax state: columns 2t and 2t + 1 of every 8-query tile
-  float m[NT][2], l[NT][2];
-  float off[NT][NG][2];        // sum p (b + 8a) - 24 sum p'
+  float m[NT][2], l[NT][2];    // reference of the exponentials, sum
+  float ref[NT][2];            // m - 60, finite
+  float off[NT][NG][2];        // sum p (b + 8a) 2^60
+  float mid[NT][NG][4];        // -8 sum p' (as o)
   float o[NT][NG][4][4];
   uint32_t qf[NT][NG][8];      // query fragments
   float X[NT][NG][2];          // group sums of the queries of columns 2t, 2t + 1
 
   __device__ AdWarp(const AdParams& pp, uint8_t* smem)
       : p(pp), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), g(lane >> 2), t(lane & 3), hbs(pp.kv_heads * pp.qblocks) {
-    ring = smem + warp * kAdStages * Gm::kStage;
-    merge = reinterpret_cast<float*>(smem + Gm::kRing);
-    bars = reinterpret_cast<uint64_t*>(smem + Gm::kRing + kAdWarps / 2 * Gm::kMerge) + warp * kAdStages;
+    ring = smem + warp * Gm::kWarp;
+    head = reinterpret_cast<float*>(ring + Gm::kRing);
+    info = reinterpret_cast<AdInfo*>(smem + Gm::kInfo);
+    bars = reinterpret_cast<uint64_t*>(smem + Gm::kBars) + warp * Gm::kStages;
   }
 
-  // tile range of this warp in the segment of steps [a, b)
-  __device__ __forceinline__ void run(int len, int a, int b, int& lo, int& hi) const {
-    const int t0 = a * kAdStepTiles, t1 = min(b * kAdStepTiles, (len + kKvTile - 1) / kKvTile);
-    const int per = (t1 - t0 + kAdWarps - 1) / kAdWarps;
-    lo = min(t1, t0 + warp * per);
-    hi = min(t1, lo + per);
-  }
-
-  // the next segment; false at the end of the block's range
-  __device__ __forceinline__ bool next(AdCursor& c, int& seq, int& hb, int& len, int& a, int& b) const {
-    if (c.left <= 0) return false;
-    seq = c.seq;
-    hb = c.hb;
-    len = c.len;
-    a = c.step;
-    b = static_cast<int>(min(static_cast<long long>(c.steps), a + c.left));
-    c.left -= b - a;
-    c.step = 0;
-    if (b == c.steps && c.left > 0 && ++c.hb == hbs) {
-      c.hb = 0;
-      do {
-        if (++c.seq >= p.seqs) {  // not reached while the lengths stay as they are
-          c.left = 0;
-          return true;
+  // the range's next part with tiles; false at its end
+  __device__ __forceinline__ bool next(AdCursor& c, AdPart& r) const {
+    while (c.x < c.end) {
+      const long long pair_end = c.pair_x + c.tiles + kAdPairCost, end = min(c.end, pair_end);
+      r.seq = c.seq;
+      r.hb = c.hb;
+      r.len = c.len;
+      r.tiles = c.tiles;
+      r.pair_x = c.pair_x;
+      r.a = max(0, static_cast<int>(c.x - c.pair_x) - kAdPairCost);
+      r.b = max(0, static_cast<int>(end - c.pair_x) - kAdPairCost);
+      c.x = end;
+      if (end == pair_end && end < c.end) {
+        c.pair_x = pair_end;
+        if (++c.hb == hbs) {
+          c.hb = 0;
+          do {
+            if (++c.seq >= p.seqs) {  // not reached while the lengths stay as they are
+              c.x = c.end;
+              break;
+            }
+            c.len = ad_len(p, c.seq);
+          } while (c.len == 0);
+          c.tiles = (c.len + kKvTile - 1) / kKvTile;
         }
-        c.len = ad_len(p, c.seq);
-      } while (c.len == 0);
-      c.steps = (c.len + kAdStep - 1) / kAdStep;
+      }
+      if (r.a < r.b) {
+        r.kvh = p.qblocks == 1 ? r.hb : r.hb / p.qblocks;
+        return true;
+      }
     }
-    return true;
+    return false;
   }
 
-  // Copies of tiles [lo, lo + n) (n <= kAdStepTiles) into ring slot `slot`: a lane per tile.
+  // Copies of tiles [lo, lo + n) (n <= kTake) of a head into ring slot `slot`: a lane per tile.
   // A bad page's tile is not copied; the bits of those that are come back.
-  __device__ __forceinline__ uint32_t fetch(int seq, int hb, int lo, int n, uint32_t slot) {
+  __device__ __forceinline__ uint32_t fetch(const AdPart& r, int lo, int n, uint32_t slot) {
+    auto page_of = [&](uint32_t tile) { return static_cast<int>((static_cast<uint64_t>(tile) * p.tiles_magic) >> 32); };
+    if (lo == r.a || page_of(lo + n - 1) >= page0 + 32) {
+      page0 = page_of(lo);
+      pages = page0 + lane < p.width ? __ldg(p.table + static_cast<long long>(r.seq) * p.width + page0 + lane) : -1;
+    }
+    const int tile = lo + lane, at = page_of(tile);
+    const int page = __shfl_sync(0xffffffffu, pages, (at - page0) & 31);
     const uint8_t* src = nullptr;
     if (lane < n) {
-      const int tpp = p.page_tokens / kKvTile, tile = lo + lane;
-      const int page = __ldg(p.table + static_cast<long long>(seq) * p.width + tile / tpp);
       if (page >= 0 && page < p.pages)
         src = p.cache + page * p.page_bytes +
-              (static_cast<long long>(hb / p.qblocks) * tpp + tile % tpp) * static_cast<long long>(Gm::kTile);
+              static_cast<long long>(r.kvh * p.page_tiles + (tile - at * p.page_tiles)) * Gm::kTile;
       else
         kv_error(p.err, FMOE_DEVERR_BAD_PAGE);
     }
@@ -199,8 +255,8 @@ struct AdWarp {
   }
 
   // query fragments and group sums of (sequence, head, query block); fresh softmax state
-  __device__ __forceinline__ void start(int seq, int hb) {
-    const int kvh = hb / p.qblocks, q0 = (hb % p.qblocks) * 8 * NT;
+  __device__ __forceinline__ void start(int seq, int kvh, int qb) {
+    const int q0 = qb * 8 * NT;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qi = q0 + nt * 8 + g;
@@ -210,16 +266,18 @@ struct AdWarp {
       for (int n = 0; n < NG; ++n) {
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
         const uint4 a = live ? __ldg(src + n * 8 + 2 * t) : z, b = live ? __ldg(src + n * 8 + 2 * t + 1) : z;
-        // channels (i, i + 4) of a word's eight in one register, as the codes' pairs
+        // channels (i, i + 4) of a word's eight in one register, as the codes' pairs, times
+        // 2^60 (even i) or 2^56: an exponent, exact
         const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          qf[nt][n][4 * w] = __byte_perm(x[4 * w], x[4 * w + 2], 0x5410);
-          qf[nt][n][4 * w + 1] = __byte_perm(x[4 * w], x[4 * w + 2], 0x7632);
-          qf[nt][n][4 * w + 2] = __byte_perm(x[4 * w + 1], x[4 * w + 3], 0x5410);
-          qf[nt][n][4 * w + 3] = __byte_perm(x[4 * w + 1], x[4 * w + 3], 0x7632);
-        }
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t u = x[4 * w + i], v = x[4 * w + 2 + i];
+            qf[nt][n][4 * w + 2 * i] = pack_bf16(bf16_lo(u) * kAdUp, bf16_lo(v) * kAdUp);
+            qf[nt][n][4 * w + 2 * i + 1] = pack_bf16(bf16_hi(u) * kAdUpHigh, bf16_hi(v) * kAdUpHigh);
+          }
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum += bf16_lo(x[i]) + bf16_hi(x[i]);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -227,6 +285,7 @@ struct AdWarp {
         X[nt][n][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
         X[nt][n][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
         off[nt][n][0] = off[nt][n][1] = 0.f;
+        mid[nt][n][0] = mid[nt][n][1] = mid[nt][n][2] = mid[nt][n][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -235,23 +294,38 @@ struct AdWarp {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         m[nt][c] = -INFINITY;
+        ref[nt][c] = -kAdLog;
         l[nt][c] = 0.f;
       }
     }
   }
 
-  // tiles in ring slot `slot`: n of them, those of `ok` copied; key0 = the first's token
+  // The (scale, bias) words of a tile's rows from `lim` on as zeros: what lies behind a
+  // sequence or on a page left out may be anything, a NaN too.
+  __device__ __forceinline__ void blank(uint8_t* tile, int lim) const {
+    for (int i = max(0, lim) * NG + lane; i < kKvTile * NG; i += 32) {
+      reinterpret_cast<uint32_t*>(tile + Kv::kOffKs)[i] = 0u;
+      reinterpret_cast<uint32_t*>(tile + Kv::kOffVs)[i] = 0u;
+    }
+    fence_proxy_async_smem();  // the slot's next copy comes behind these
+    __syncwarp();
+  }
+
+  // n tiles in ring slot `slot`, those of `ok` copied; key0 = the first's token
   __device__ __forceinline__ void step(uint32_t slot, int n, uint32_t ok, int key0, int len) {
-    const uint8_t* base = ring + slot * Gm::kStage;
+    constexpr int kTake = Gm::kTake;
+    uint8_t* base = ring + slot * Gm::kStage;
     const int r = g ^ ((g >> 1) & 1);  // row order that spreads the value rows over the banks
-    float S[kAdStepTiles][NT][4];
+    float S[kTake][NT][4];
     float mx[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
-    for (int ti = 0; ti < kAdStepTiles; ++ti) {
+    for (int ti = 0; ti < kTake; ++ti) {
       if (ti < n) {
-        const uint8_t* tile = base + ti * Gm::kTile;
+        uint8_t* tile = base + ti * Gm::kTile;
+        const int lim = (ok >> ti) & 1 ? len - key0 - ti * kKvTile : 0;  // rows of the sequence
+        if (lim < kKvTile) blank(tile, lim);
         uint32_t w0[2 * NG], w1[2 * NG], a0[NG], a1[NG];
         load_words<2 * NG>(w0, tile + r * Kv::kRow + t * (8 * NG));
         load_words<2 * NG>(w1, tile + (r + 8) * Kv::kRow + t * (8 * NG));
@@ -259,112 +333,112 @@ struct AdWarp {
         load_words<NG>(a1, tile + Kv::kOffKs + (r + 8) * (4 * NG));
         float acc[NT][NG][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) acc[nt][gr][0] = acc[nt][gr][1] = acc[nt][gr][2] = acc[nt][gr][3] = 0.f;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
-            const uint32_t x0 = w0[(s >> 1) * NG + gr], x1 = w1[(s >> 1) * NG + gr];
-            const int i = 2 * (s & 1);
-            const uint32_t f0 = code_pair(x0, i), f1 = code_pair(x1, i), f2 = code_pair(x0, i + 1), f3 = code_pair(x1, i + 1);
+            const uint32_t x0 = w0[j * NG + gr], x1 = w1[j * NG + gr], y0 = x0 >> 8, y1 = x1 >> 8;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16(acc[nt][gr], f0, f1, f2, f3, qf[nt][gr][2 * s], qf[nt][gr][2 * s + 1]);
+            for (int i = 0; i < 4; i += 2) {
+              const uint32_t f0 = code_pair(x0, y0, i), f1 = code_pair(x1, y1, i);
+              const uint32_t f2 = code_pair(x0, y0, i + 1), f3 = code_pair(x1, y1, i + 1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t q0 = qf[nt][gr][4 * j + i], q1 = qf[nt][gr][4 * j + i + 1];
+                if (i + j == 0)
+                  mma_bf16_first(acc[nt][gr], f0, f1, f2, f3, q0, q1);
+                else
+                  mma_bf16(acc[nt][gr], f0, f1, f2, f3, q0, q1);
+              }
+            }
           }
+        const float in0 = r < lim ? 0.f : -INFINITY, in1 = r + 8 < lim ? 0.f : -INFINITY;
+        float c0[NG], c1[NG], d0[NG], d1[NG];
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          c0[gr] = sb_scale(a0[gr]) * p.scale_up;
+          c1[gr] = sb_scale(a1[gr]) * p.scale_up;
+          d0[gr] = sb_bias(a0[gr]) * p.scale_log2;
+          d1[gr] = sb_bias(a1[gr]) * p.scale_log2;
         }
-        const int key = key0 + ti * kKvTile + r;
-        const bool in = (ok >> ti) & 1, v0 = in && key < len, v1 = in && key + 8 < len;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+          float s0 = in0, s1 = in0, s2 = in1, s3 = in1;
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
-            const float c0 = sb_scale(a0[gr]) * (16.f * p.scale_log2), c1 = sb_scale(a1[gr]) * (16.f * p.scale_log2);
-            const float d0 = fmaf(sb_bias(a0[gr]), p.scale_log2, -c0), d1 = fmaf(sb_bias(a1[gr]), p.scale_log2, -c1);
-            s0 = fmaf(c0, acc[nt][gr][0], fmaf(d0, X[nt][gr][0], s0));
-            s1 = fmaf(c0, acc[nt][gr][1], fmaf(d0, X[nt][gr][1], s1));
-            s2 = fmaf(c1, acc[nt][gr][2], fmaf(d1, X[nt][gr][0], s2));
-            s3 = fmaf(c1, acc[nt][gr][3], fmaf(d1, X[nt][gr][1], s3));
+            s0 = fmaf(c0[gr], acc[nt][gr][0], fmaf(d0[gr], X[nt][gr][0], s0));
+            s1 = fmaf(c0[gr], acc[nt][gr][1], fmaf(d0[gr], X[nt][gr][1], s1));
+            s2 = fmaf(c1[gr], acc[nt][gr][2], fmaf(d1[gr], X[nt][gr][0], s2));
+            s3 = fmaf(c1[gr], acc[nt][gr][3], fmaf(d1[gr], X[nt][gr][1], s3));
           }
-          S[ti][nt][0] = v0 ? s0 : -INFINITY;
-          S[ti][nt][1] = v0 ? s1 : -INFINITY;
-          S[ti][nt][2] = v1 ? s2 : -INFINITY;
-          S[ti][nt][3] = v1 ? s3 : -INFINITY;
-          mx[nt][0] = fmaxf(mx[nt][0], fmaxf(S[ti][nt][0], S[ti][nt][2]));
-          mx[nt][1] = fmaxf(mx[nt][1], fmaxf(S[ti][nt][1], S[ti][nt][3]));
+          S[ti][nt][0] = s0, S[ti][nt][1] = s1, S[ti][nt][2] = s2, S[ti][nt][3] = s3;
+          mx[nt][0] = fmaxf(mx[nt][0], fmaxf(s0, s2));
+          mx[nt][1] = fmaxf(mx[nt][1], fmaxf(s1, s3));
         }
       }
     }
-    // the running maximum per query and the rescaling of what was summed under the old one
-    bool moved = false;
-    float al[NT][2];
+    // a maximum that passed its reference: what was summed is rescaled to the new one
+    bool far = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float x = mx[nt][c];
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        const float now = fmaxf(m[nt][c], x);
-        moved |= now > m[nt][c];
-        al[nt][c] = ex2(m[nt][c] - (now == -INFINITY ? 0.f : now));
-        m[nt][c] = now;
-        mx[nt][c] = now == -INFINITY ? 0.f : now;  // the reference: keys that are all left out have weight 0
-      }
-    if (__any_sync(0xffffffffu, moved)) {
+    for (int nt = 0; nt < NT; ++nt) far |= mx[nt][0] - kAdSlack > m[nt][0] || mx[nt][1] - kAdSlack > m[nt][1];
+    if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        float al[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) l[nt][c] *= al[nt][c];
+        for (int c = 0; c < 2; ++c) {
+          float x = mx[nt][c];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const bool up = x - kAdSlack > m[nt][c];
+          al[c] = up ? ex2(m[nt][c] - x) : 1.f;
+          if (up) {
+            m[nt][c] = x;
+            ref[nt][c] = x - kAdLog;
+          }
+          l[nt][c] *= al[c];
+        }
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-          off[nt][gr][0] *= al[nt][0];
-          off[nt][gr][1] *= al[nt][1];
+          off[nt][gr][0] *= al[0];
+          off[nt][gr][1] *= al[1];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mid[nt][gr][e] *= al[e & 1];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][gr][i][e] *= al[nt][e & 1];
+            for (int e = 0; e < 4; ++e) o[nt][gr][i][e] *= al[e & 1];
         }
       }
     }
 #pragma unroll
-    for (int ti = 0; ti < kAdStepTiles; ++ti) {
+    for (int ti = 0; ti < kTake; ++ti) {
       if (ti < n) {
         const uint8_t* tile = base + ti * Gm::kTile;
         uint32_t b0[NG], b1[NG];
         load_words<NG>(b0, tile + Kv::kOffVs + r * (4 * NG));
         load_words<NG>(b1, tile + Kv::kOffVs + (r + 8) * (4 * NG));
-        const int key = key0 + ti * kKvTile + r;
-        const bool in = (ok >> ti) & 1, v0 = in && key < len, v1 = in && key + 8 < len;
         uint32_t f[NT][NG][2];
 #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            S[ti][nt][e] = ex2(S[ti][nt][e] - ref[nt][e & 1]);
+            l[nt][e & 1] += S[ti][nt][e];
+          }
+#pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-          // the words of a key left out may be anything, a NaN too: as zeros they add nothing
-          const uint32_t x0 = v0 ? b0[gr] : 0u, x1 = v1 ? b1[gr] : 0u;
-          const float a0 = sb_scale(x0), a1 = sb_scale(x1);
-          const float c0 = fmaf(8.f, a0, sb_bias(x0)), c1 = fmaf(8.f, a1, sb_bias(x1));
+          const float a0 = sb_scale(b0[gr]), a1 = sb_scale(b1[gr]);
+          const float c0 = fmaf(8.f, a0, sb_bias(b0[gr])), c1 = fmaf(8.f, a1, sb_bias(b1[gr]));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (gr == 0) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                S[ti][nt][e] = ex2(S[ti][nt][e] - mx[nt][e & 1]);
-                l[nt][e & 1] += S[ti][nt][e];
-              }
-            }
             const float* P = S[ti][nt];
-            const uint32_t y0 = pack_bf16(P[0] * a0, P[1] * a0), y1 = pack_bf16(P[2] * a1, P[3] * a1);
-            float u0 = off[nt][gr][0], u1 = off[nt][gr][1];
-            u0 = fmaf(P[0], c0, fmaf(-24.f, bf16_lo(y0), u0));
-            u1 = fmaf(P[1], c0, fmaf(-24.f, bf16_hi(y0), u1));
-            u0 = fmaf(P[2], c1, fmaf(-24.f, bf16_lo(y1), u0));
-            u1 = fmaf(P[3], c1, fmaf(-24.f, bf16_hi(y1), u1));
-            off[nt][gr][0] = u0;
-            off[nt][gr][1] = u1;
-            f[nt][gr][0] = movmatrix_trans(y0);
-            f[nt][gr][1] = movmatrix_trans(y1);
+            off[nt][gr][0] = fmaf(P[2], c1, fmaf(P[0], c0, off[nt][gr][0]));
+            off[nt][gr][1] = fmaf(P[3], c1, fmaf(P[1], c0, off[nt][gr][1]));
+            f[nt][gr][0] = movmatrix_trans(pack_bf16(P[0] * a0, P[1] * a0));
+            f[nt][gr][1] = movmatrix_trans(pack_bf16(P[2] * a1, P[3] * a1));
+            constexpr uint32_t kMid = 0x80088008u;  // -8 2^-133
+            mma_bf16(mid[nt][gr], kMid, kMid, kMid, kMid, f[nt][gr][0], f[nt][gr][1]);
           }
         }
         // value words of rows 2t, 2t + 1 of each half (in the row order above)
@@ -379,9 +453,10 @@ struct AdWarp {
           // four codes of one row in the low half, the other row's in the high half
           const uint32_t x0 = __byte_perm(w0[gr], w1[gr], 0x5410), x1 = __byte_perm(w0[gr], w1[gr], 0x7632);
           const uint32_t x2 = __byte_perm(w2[gr], w3[gr], 0x5410), x3 = __byte_perm(w2[gr], w3[gr], 0x7632);
+          const uint32_t y0 = x0 >> 8, y1 = x1 >> 8, y2 = x2 >> 8, y3 = x3 >> 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t e0 = code_pair(x0, i), e1 = code_pair(x1, i), e2 = code_pair(x2, i), e3 = code_pair(x3, i);
+            const uint32_t e0 = code_pair(x0, y0, i), e1 = code_pair(x1, y1, i), e2 = code_pair(x2, y2, i), e3 = code_pair(x3, y3, i);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][gr][i], e0, e1, e2, e3, f[nt][gr][0], f[nt][gr][1]);
           }
@@ -411,7 +486,7 @@ struct AdWarp {
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) {
-          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);  // (2^60 in it)
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) off[nt][gr][c] += __shfl_xor_sync(0xffffffffu, off[nt][gr][c], x);
         }
@@ -421,7 +496,11 @@ struct AdWarp {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][gr][i][e] = fmaf(16.f, o[nt][gr][i][e], off[nt][gr][e & 1]);
+          for (int e = 0; e < 4; ++e)
+            o[nt][gr][i][e] = fmaf(o[nt][gr][i][e], i & 1 ? kAdDown / 16.f : kAdDown,
+                                   fmaf(mid[nt][gr][e], kAdDown, off[nt][gr][e & 1] * 0x1p-60f));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) l[nt][c] *= 0x1p-60f;
     }
   }
 
@@ -467,16 +546,37 @@ struct AdWarp {
     }
   }
 
-  // the block's warps into warp 0, in two rounds
-  __device__ __forceinline__ void join() {
-    __syncthreads();
-    if (warp >= 2) put(merge + (warp - 2) * (Gm::kMerge / 4));
-    __syncthreads();
-    if (warp < 2) add(merge + warp * (Gm::kMerge / 4));
-    __syncthreads();
-    if (warp == 1) put(merge);
-    __syncthreads();
-    if (warp == 0) add(merge);
+  __device__ __forceinline__ void get(const float* src) {
+    int k = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = src[32 * k++ + lane];
+        l[nt][c] = src[32 * k++ + lane];
+      }
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][gr][i][e] = src[32 * k++ + lane];
+    }
+  }
+
+  // The parts of the pair that warp v ended, or began without ending, joined with those of the
+  // warps before it; whether the pair began in this block.
+  __device__ __forceinline__ const float* part_of(int v, bool tail) const {
+    const float* own = reinterpret_cast<const float*>(reinterpret_cast<uint8_t*>(info) - Gm::kInfo + v * Gm::kWarp);
+    return tail ? own : own + Gm::kRing / 4;
+  }
+  __device__ __forceinline__ bool join(int v, bool tail) {
+    get(part_of(v, tail));
+    while (!tail && --v >= 0) {
+      tail = info[v].tail;
+      if (tail || (info[v].head && !info[v].head_ends)) add(part_of(v, tail));
+    }
+    return tail;
   }
 
   __device__ __forceinline__ void write_out(int seq, int hb) const {
@@ -520,13 +620,13 @@ struct AdWarp {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAdThreads, 2) attn_decode_kernel(const __grid_constant__ AdParams p) {
+__global__ void __launch_bounds__(kAdThreads, AdGeom<D, NT>::kBlocks) attn_decode_kernel(const __grid_constant__ AdParams p) {
   using Gm = AdGeom<D, NT>;
   extern __shared__ __align__(128) uint8_t ad_smem[];
   AdWarp<D, NT> W(p, ad_smem);
   const int lane = W.lane;
   if (lane == 0) {
-    for (int i = 0; i < kAdStages; ++i) mbar_init(&W.bars[i], 1);
+    for (int i = 0; i < Gm::kStages; ++i) mbar_init(&W.bars[i], 1);
     mbar_init_fence();
   }
   __syncwarp();
@@ -542,111 +642,131 @@ __global__ void __launch_bounds__(kAdThreads, 2) attn_decode_kernel(const __grid
         reinterpret_cast<uint4*>(p.out + static_cast<long long>(s) * p.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
 
-  // the block's range of the line of units (every warp finds it for itself)
+  // the warp's range of the line
+  auto cost = [&](int len) { return len > 0 ? (len + kKvTile - 1) / kKvTile + kAdPairCost : 0; };
   long long total = 0;
-  for (int s = lane; s < p.seqs; s += 32) total += (ad_len(p, s) + kAdStep - 1) / kAdStep;
+  for (int s = lane; s < p.seqs; s += 32) total += cost(ad_len(p, s));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
   total *= W.hbs;
-  const long long blocks = min(static_cast<long long>(gridDim.x), total);
-  const long long bid = blockIdx.x;
-  if (threadIdx.x == 0) p.rec[bid].first = -1;
-  if (bid >= blocks) return;
-  const long long u0 = total * bid / blocks, u1 = total * (bid + 1) / blocks;
-  AdCursor cur;
-  cur.left = u1 - u0;
-  long long base = 0;  // units before the sequences of this round
-  for (int s0 = 0;; s0 += 32) {
-    const int len = s0 + lane < p.seqs ? ad_len(p, s0 + lane) : 0;
-    const long long mine = static_cast<long long>((len + kAdStep - 1) / kAdStep) * W.hbs;
-    long long upto = mine;
+  const long long warps = min(static_cast<long long>(gridDim.x) * kAdWarps, total);
+  const long long me = static_cast<long long>(blockIdx.x) * kAdWarps + W.warp;
+  AdInfo mine{};
+  if (threadIdx.x == 0) p.rec[blockIdx.x].first = -1;
+  if (me < warps) {
+    AdCursor cur;
+    cur.x = total * me / warps;
+    cur.end = total * (me + 1) / warps;
+    long long base = 0;  // the line before the sequences of this round
+    for (int s0 = 0;; s0 += 32) {
+      const int len = s0 + lane < p.seqs ? ad_len(p, s0 + lane) : 0;
+      const long long own = static_cast<long long>(cost(len)) * W.hbs;
+      long long upto = own;
 #pragma unroll
-    for (int x = 1; x < 32; x *= 2) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, x);
-      if (lane >= x) upto += y;
+      for (int x = 1; x < 32; x *= 2) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, x);
+        if (lane >= x) upto += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, base + upto > cur.x);
+      if (past != 0) {
+        const int who = __ffs(past) - 1;
+        const long long from = base + __shfl_sync(0xffffffffu, upto - own, who);
+        cur.seq = s0 + who;
+        cur.len = __shfl_sync(0xffffffffu, len, who);
+        cur.tiles = (cur.len + kKvTile - 1) / kKvTile;
+        cur.hb = static_cast<int>((cur.x - from) / (cur.tiles + kAdPairCost));
+        cur.pair_x = from + static_cast<long long>(cur.hb) * (cur.tiles + kAdPairCost);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, upto, 31);
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, base + upto > u0);
-    if (past != 0) {
-      const int who = __ffs(past) - 1;
-      const long long in = u0 - (base + __shfl_sync(0xffffffffu, upto - mine, who));
-      cur.seq = s0 + who;
-      cur.len = __shfl_sync(0xffffffffu, len, who);
-      cur.steps = (cur.len + kAdStep - 1) / kAdStep;
-      cur.hb = static_cast<int>(in / cur.steps);
-      cur.step = static_cast<int>(in % cur.steps);
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, upto, 31);
-  }
 
-  // the warp's copies run up to kAdStages steps ahead of its arithmetic, over the ends of
-  // segments too
-  AdCursor ahead = cur;
-  int fs = 0, fhb = 0, flen = 0, fa = 0, fb = 0, flo = 0, fhi = 0;
-  bool more = true;
-  uint32_t issued = 0, done = 0, oks = 0;  // oks: 4 bits per ring slot
-  auto refill = [&]() {
-    while (more && issued - done < kAdStages) {
-      while (flo >= fhi) {
-        if (!W.next(ahead, fs, fhb, flen, fa, fb)) {
-          more = false;
-          return;
+    // copies run up to kStages steps ahead of the arithmetic, over the ends of parts too
+    AdCursor ahead = cur;
+    AdPart fr{};
+    int flo = 0;
+    bool more = true;
+    uint32_t issued = 0, done = 0, oks = 0;  // oks: 4 bits per ring slot
+    auto refill = [&]() {
+      while (more && issued - done < Gm::kStages) {
+        if (flo >= fr.b) {
+          if (!W.next(ahead, fr)) {
+            more = false;
+            return;
+          }
+          flo = fr.a;
         }
-        W.run(flen, fa, fb, flo, fhi);
+        const uint32_t slot = issued % Gm::kStages;
+        const int n = min(Gm::kTake, fr.b - flo);
+        oks = (oks & ~(0xFu << (4 * slot))) | (W.fetch(fr, flo, n, slot) << (4 * slot));
+        flo += n;
+        ++issued;
       }
-      const uint32_t slot = issued % kAdStages;
-      const int n = min(kAdStepTiles, fhi - flo);
-      oks = (oks & ~(0xFu << (4 * slot))) | (W.fetch(fs, fhb, flo, n, slot) << (4 * slot));
-      flo += n;
-      ++issued;
-    }
-  };
-  refill();
-  int seq, hb, len, a, b;
-  bool begun_before = cur.step > 0;
-  while (W.next(cur, seq, hb, len, a, b)) {
-    W.start(seq, hb);
-    int lo, hi;
-    W.run(len, a, b, lo, hi);
-    while (lo < hi) {
-      const int n = min(kAdStepTiles, hi - lo);
-      const uint32_t slot = done % kAdStages;
-      W.wait(slot, (done / kAdStages) & 1u);
-      W.step(slot, n, (oks >> (4 * slot)) & 0xFu, lo * kKvTile, len);
-      __syncwarp();
-      ++done;
-      refill();
-      lo += n;
-    }
-    W.finish();
-    W.join();
-    const bool ends = b == (len + kAdStep - 1) / kAdStep;
-    if (W.warp == 0) {
-      if (ends && !begun_before) {
-        W.write_out(seq, hb);
+    };
+    refill();
+    AdPart r;
+    while (W.next(cur, r)) {
+      W.start(r.seq, r.kvh, r.hb - r.kvh * p.qblocks);
+      for (int lo = r.a; lo < r.b; lo += Gm::kTake) {
+        const uint32_t slot = done % Gm::kStages;
+        W.wait(slot, (done / Gm::kStages) & 1u);
+        W.step(slot, min(Gm::kTake, r.b - lo), (oks >> (4 * slot)) & 0xFu, lo * kKvTile, r.len);
+        __syncwarp();
+        ++done;
+        refill();
+      }
+      W.finish();
+      mine.some = 1;
+      if (r.a > 0) {
+        W.put(W.head);
+        mine.head = 1;
+        mine.head_ends = r.b == r.tiles;
+        mine.seq = r.seq;
+        mine.hb = r.hb;
+        mine.pair_x = r.pair_x;
+      } else if (r.b < r.tiles) {
+        W.put(reinterpret_cast<float*>(W.ring));  // the range ends here: its copies are read
+        mine.tail = 1;
       } else {
-        W.write_part(ends ? 0 : 1);
+        W.write_out(r.seq, r.hb);
       }
     }
-    if (ends && begun_before && threadIdx.x == 0) {
-      // the segment began in the block that holds its first unit: unit u lies in block
-      // ((u + 1) blocks - 1) / total
-      const long long end = u1 - cur.left;  // one past the segment's last unit
-      const long long begin = end - (len + kAdStep - 1) / kAdStep;
-      AdRecord r;
-      r.first = static_cast<int>(((begin + 1) * blocks - 1) / total);
-      r.seq = seq;
-      r.head0 = (hb / p.qblocks) * p.group + (hb % p.qblocks) * 8 * NT;
-      r.queries = min(8 * NT, p.group - (hb % p.qblocks) * 8 * NT);
-      p.rec[bid] = r;
+  }
+  if (lane == 0) W.info[W.warp] = mine;
+  __syncthreads();
+  // pairs that end in this warp and began before it
+  if (mine.head && mine.head_ends) {
+    if (W.join(W.warp, false)) {
+      W.write_out(mine.seq, mine.hb);
+    } else {
+      W.write_part(0);
+      if (lane == 0) {
+        // the place u of the line lies in the range of warp ((u + 1) warps - 1) / total
+        const int kvh = mine.hb / p.qblocks, q0 = (mine.hb - kvh * p.qblocks) * 8 * NT;
+        AdRecord rec;
+        rec.first = static_cast<int>(((mine.pair_x + kAdPairCost + 1) * warps - 1) / total) / kAdWarps;
+        rec.seq = mine.seq;
+        rec.head0 = kvh * p.group + q0;
+        rec.queries = min(8 * NT, p.group - q0);
+        p.rec[blockIdx.x] = rec;
+      }
     }
-    begun_before = false;
+  }
+  // the pair that goes on behind the block
+  if (W.warp == kAdWarps - 1) {
+    int v = W.warp;
+    while (v > 0 && !W.info[v].some) --v;
+    const AdInfo& last = W.info[v];
+    if (last.tail || (last.head && !last.head_ends)) {
+      W.join(v, last.tail);
+      W.write_part(1);
+    }
   }
 }
 
-// Joins the segments of a (sequence, head) that blocks first .. b hold: block (b, query).
-// Warps take every fourth part, a lane D/32 channels.
-constexpr int kAjWarps = 4;
+// Joins the parts of a pair that blocks first .. b hold: block (b, query).  Warps take every
+// eighth part, a lane 4 (D = 64: 2) channels.
+constexpr int kAjWarps = 8;
 template <int D, int NT>
 __global__ void __launch_bounds__(kAjWarps * 32) attn_join_kernel(const __grid_constant__ AdParams p) {
   constexpr int C = D / 32;
@@ -659,7 +779,7 @@ __global__ void __launch_bounds__(kAjWarps * 32) attn_join_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int last = blockIdx.x;
   auto row = [&](int b) { return (static_cast<long long>(b) * 2 + (b == last ? 0 : 1)) * (8 * NT) + qi; };
-  // the maximum over the parts, then the weighted sums
+  // the largest reference, then the weighted sums
   float m = -INFINITY;
   for (int b = r.first + lane; b <= last; b += 32) m = fmaxf(m, p.part_ml[2 * row(b)]);
 #pragma unroll
@@ -668,17 +788,25 @@ __global__ void __launch_bounds__(kAjWarps * 32) attn_join_kernel(const __grid_c
   float l = 0.f, o[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int b = r.first + warp; b <= last; b += kAjWarps) {
     const long long at = row(b);
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+    float v[C];
+    if constexpr (C == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p.part + at * D + 4 * lane);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(p.part + at * D + 2 * lane);
+      v[0] = x.x, v[1] = x.y;
+    }
     const float w = ex2(ml.x - ref);
     l = fmaf(w, ml.y, l);
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = fmaf(w, p.part[at * D + 32 * c + lane], o[c]);
+    for (int c = 0; c < C; ++c) o[c] = fmaf(w, v[c], o[c]);
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) so[warp][32 * c + lane] = o[c];
+  for (int c = 0; c < C; ++c) so[warp][C * lane + c] = o[c];
   if (lane == 0) sl[warp] = l;
   __syncthreads();
   const int ch = threadIdx.x;
