@@ -102,9 +102,13 @@ fmoe_status decode(AdParams& p, int sms, int device, int64_t places, void* strea
   int64_t blocks = sms * AdGeom<D, NT>::kBlocks;
   if (blocks > kAdMaxBlocks) blocks = kAdMaxBlocks;
   if (blocks * kAdWarps > places) blocks = (places + kAdWarps - 1) / kAdWarps;  // a warp takes one place at least
+  p.blocks = (int)blocks;
   fmoe_status st = launch(attn_decode_kernel<D, NT>, dim3((unsigned)blocks), kAdThreads, smem, stream, p);
   if (st != FMOE_OK) return st;
-  return launch(attn_join_kernel<D, NT>, dim3((unsigned)blocks, 8 * NT), kAjWarps * 32, 0, stream, p);
+  // a pair's parts lie in two blocks at least: as many (pair, query) items as there can be
+  const int64_t items = blocks * (p.group < 8 * NT ? p.group : 8 * NT);
+  return blocks == 1 ? FMOE_OK
+                     : launch(attn_join_kernel<D, NT>, dim3((unsigned)(items < sms ? items : sms)), kAjWarps * 32, 0, stream, p);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

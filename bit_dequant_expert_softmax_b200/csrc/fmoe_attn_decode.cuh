@@ -34,6 +34,8 @@
 // the sums are rescaled a few times per pair and not at every new maximum.
 #pragma once
 
+#include <type_traits>
+
 #include "fmoe_kv.cuh"
 
 namespace fmoe {
@@ -67,7 +69,7 @@ struct AdParams {
   uint32_t* err;
   float scale_log2, scale_up;  // scale * log2(e); the same times 2^73
   unsigned long long tiles_magic;  // ceil(2^32 / page_tiles)
-  int page_tiles, width, seqs, q_heads, kv_heads, group, qblocks, page_tokens;
+  int blocks, page_tiles, width, seqs, q_heads, kv_heads, group, qblocks, page_tokens;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -82,14 +84,14 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -99,33 +101,17 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w8, int i) {
   return (i < 2 ? w : w8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
 
+// Quotient of numbers that are hardly ever past 32 bits.
+__device__ __forceinline__ long long div64(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 __device__ __forceinline__ int ad_len(const AdParams& p, int s) {
   const int len = __ldg(p.lens + s);
   const long long most = static_cast<long long>(p.width) * p.page_tokens;
   return len <= 0 ? 0 : len > most ? static_cast<int>(most) : len;
 }
-
-#ifndef AD_T
-#define AD_T 3
-#define AD_S 2
-#define AD_B 3
-#endif
-template <int D, int NT>
-struct AdGeom {
-  static constexpr int kTake = NT == 1 ? AD_T : 2;    // tiles a warp takes at once
-  static constexpr int kStages = NT == 1 ? AD_S : 3;  // ring slots per warp
-  static constexpr int kBlocks = NT == 1 ? AD_B : 2;  // blocks per SM
-  static constexpr int kTile = KvGeom<D>::kTileBytes;
-  static constexpr int kStage = kTake * kTile;
-  static constexpr int kRegs = 16 * KvGeom<D>::kGroups * NT;  // output floats of a thread
-  static constexpr int kState = 32 * (kRegs + 4 * NT) * 4;    // a warp's sums, bytes
-  static constexpr int kRing = kStages * kStage;              // of a warp
-  static constexpr int kWarp = kRing + kState;                // its ring and the part it began with
-  static constexpr int kInfo = kAdWarps * kWarp;
-  static constexpr int kBars = kInfo + kAdWarps * 32;
-  static constexpr int kSmem = kBars + kAdWarps * kStages * 8;
-  static_assert(kState <= kRing, "the part that a warp ends with goes into its ring");
-};
 
 // A warp's parts of pairs that it shares with other warps.
 struct AdInfo {
@@ -135,20 +121,42 @@ struct AdInfo {
   int seq, hb;         // the pair of `head`
   long long pair_x;    // its place in the line
 };
-static_assert(sizeof(AdInfo) == 32, "space set aside");
-
-// A warp's way along the line.
-struct AdCursor {
-  long long x, end;    // what is left of its range
-  long long pair_x;    // the current pair: its first place,
-  int seq, hb;         // sequence and (head, query block),
-  int len, tiles;      // length and tiles
-};
 
 // Tiles [a, b) of a pair.
 struct AdPart {
-  int seq, hb, kvh, len, tiles, a, b;
-  long long pair_x;
+  long long pair_x;    // the pair's first place in the line
+  int seq, hb, kvh, len, tiles, a, b, pad;
+};
+
+// A warp's way along the line, in shared memory: it is looked at once per part, and the
+// registers are the scarcer (the sums of a warp leave room for 12 to 16 warps on an SM).
+constexpr int kAdParts = 4;
+struct AdControl {
+  AdPart part[kAdParts];  // those between the copies and the arithmetic
+  long long x, end;       // what is left of the range
+  long long pair_x;       // the current pair: its first place,
+  int seq, hb;            // sequence and (head, query block),
+  int len, tiles;         // length and tiles
+  long long share, extra; // places of a warp, and how many warps have one more
+  AdInfo info;
+};
+
+template <int D, int NT>
+struct AdGeom {
+  static constexpr int kTake = 3;                     // tiles a warp takes at once
+  static constexpr int kStages = 2;                   // ring slots per warp
+  static constexpr int kBlocks = NT == 1 ? 3 : 2;     // blocks per SM: 168 registers a thread, or 255
+  static constexpr int kTile = KvGeom<D>::kTileBytes;
+  static constexpr int kStage = kTake * kTile;
+  static constexpr int kRegs = 16 * KvGeom<D>::kGroups * NT;  // output floats of a thread
+  static constexpr int kState = 32 * (kRegs + 4 * NT) * 4;    // a warp's sums, bytes
+  static constexpr int kRing = kStages * kStage;              // of a warp
+  static constexpr int kWarp = kRing + kState;                // its ring and the part it began with
+  static constexpr int kControl = kAdWarps * kWarp;
+  static constexpr int kBars = kControl + kAdWarps * static_cast<int>(sizeof(AdControl));
+  static constexpr int kSmem = kBars + kAdWarps * kStages * 8;
+  static_assert(kStages + 1 <= kAdParts, "parts in flight");
+  static_assert(kState <= kRing, "the part that a warp ends with goes into its ring");
 };
 
 template <int D, int NT>
@@ -161,7 +169,8 @@ struct AdWarp {
   const int hbs;               // (head, query block) pairs per sequence
   uint8_t* ring;
   float* head;                 // the part of the pair that the warp began within
-  AdInfo* info;                // of all the block's warps
+  AdControl* all;              // of the block's warps
+  AdControl* my;
   uint64_t* bars;
   bool lost = false;           // a copy's wait ran out
   int page0 = 0, pages = 0;    // page table entries page0 .. of the pair being fetched, one per lane
@@ -179,49 +188,66 @@ struct AdWarp {
       : p(pp), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), g(lane >> 2), t(lane & 3), hbs(pp.kv_heads * pp.qblocks) {
     ring = smem + warp * Gm::kWarp;
     head = reinterpret_cast<float*>(ring + Gm::kRing);
-    info = reinterpret_cast<AdInfo*>(smem + Gm::kInfo);
+    all = reinterpret_cast<AdControl*>(smem + Gm::kControl);
+    my = all + warp;
     bars = reinterpret_cast<uint64_t*>(smem + Gm::kBars) + warp * Gm::kStages;
   }
 
-  // the range's next part with tiles; false at its end
-  __device__ __forceinline__ bool next(AdCursor& c, AdPart& r) const {
-    while (c.x < c.end) {
-      const long long pair_end = c.pair_x + c.tiles + kAdPairCost, end = min(c.end, pair_end);
-      r.seq = c.seq;
-      r.hb = c.hb;
-      r.len = c.len;
-      r.tiles = c.tiles;
-      r.pair_x = c.pair_x;
-      r.a = max(0, static_cast<int>(c.x - c.pair_x) - kAdPairCost);
-      r.b = max(0, static_cast<int>(end - c.pair_x) - kAdPairCost);
-      c.x = end;
-      if (end == pair_end && end < c.end) {
-        c.pair_x = pair_end;
-        if (++c.hb == hbs) {
-          c.hb = 0;
+  // the range's next part with tiles into part[slot]; false at its end
+  __device__ __forceinline__ bool next(int slot) {
+    long long x = my->x, pair_x = my->pair_x;
+    const long long range_end = my->end;
+    int seq = my->seq, hb = my->hb, len = my->len, tiles = my->tiles;
+    bool found = false;
+    while (x < range_end && !found) {
+      const long long pair_end = pair_x + tiles + kAdPairCost, end = min(range_end, pair_end);
+      const int a = max(0, static_cast<int>(x - pair_x) - kAdPairCost), b = max(0, static_cast<int>(end - pair_x) - kAdPairCost);
+      found = a < b;
+      if (found && lane == 0) {
+        AdPart& r = my->part[slot];
+        r.pair_x = pair_x;
+        r.seq = seq;
+        r.hb = hb;
+        r.kvh = hb / p.qblocks;
+        r.len = len;
+        r.tiles = tiles;
+        r.a = a;
+        r.b = b;
+      }
+      x = end;
+      if (end == pair_end && end < range_end) {
+        pair_x = pair_end;
+        if (++hb == hbs) {
+          hb = 0;
           do {
-            if (++c.seq >= p.seqs) {  // not reached while the lengths stay as they are
-              c.x = c.end;
+            if (++seq >= p.seqs) {  // not reached while the lengths stay as they are
+              x = range_end;
               break;
             }
-            c.len = ad_len(p, c.seq);
-          } while (c.len == 0);
-          c.tiles = (c.len + kKvTile - 1) / kKvTile;
+            len = ad_len(p, seq);
+          } while (len == 0);
+          tiles = (len + kKvTile - 1) / kKvTile;
         }
       }
-      if (r.a < r.b) {
-        r.kvh = p.qblocks == 1 ? r.hb : r.hb / p.qblocks;
-        return true;
-      }
     }
-    return false;
+    __syncwarp();
+    if (lane == 0) {
+      my->x = x;
+      my->pair_x = pair_x;
+      my->seq = seq;
+      my->hb = hb;
+      my->len = len;
+      my->tiles = tiles;
+    }
+    __syncwarp();
+    return found;
   }
 
   // Copies of tiles [lo, lo + n) (n <= kTake) of a head into ring slot `slot`: a lane per tile.
   // A bad page's tile is not copied; the bits of those that are come back.
-  __device__ __forceinline__ uint32_t fetch(const AdPart& r, int lo, int n, uint32_t slot) {
+  __device__ __forceinline__ uint32_t fetch(const AdPart& r, int kvh, bool first, int lo, int n, uint32_t slot) {
     auto page_of = [&](uint32_t tile) { return static_cast<int>((static_cast<uint64_t>(tile) * p.tiles_magic) >> 32); };
-    if (lo == r.a || page_of(lo + n - 1) >= page0 + 32) {
+    if (first || page_of(lo + n - 1) >= page0 + 32) {
       page0 = page_of(lo);
       pages = page0 + lane < p.width ? __ldg(p.table + static_cast<long long>(r.seq) * p.width + page0 + lane) : -1;
     }
@@ -231,7 +257,7 @@ struct AdWarp {
     if (lane < n) {
       if (page >= 0 && page < p.pages)
         src = p.cache + page * p.page_bytes +
-              static_cast<long long>(r.kvh * p.page_tiles + (tile - at * p.page_tiles)) * Gm::kTile;
+              static_cast<long long>(kvh * p.page_tiles + (tile - at * p.page_tiles)) * Gm::kTile;
       else
         kv_error(p.err, FMOE_DEVERR_BAD_PAGE);
     }
@@ -311,10 +337,26 @@ struct AdWarp {
     __syncwarp();
   }
 
-  // n tiles in ring slot `slot`, those of `ok` copied; key0 = the first's token
+  // The n tiles in ring slot `slot`, those of `ok` copied; key0 = the first's token.  A full
+  // slot well inside the sequence goes in one piece without masks, others tile by tile.
   __device__ __forceinline__ void step(uint32_t slot, int n, uint32_t ok, int key0, int len) {
     constexpr int kTake = Gm::kTake;
     uint8_t* base = ring + slot * Gm::kStage;
+    if (n == kTake && ok == (1u << kTake) - 1 && key0 + kTake * kKvTile <= len) {
+      tiles<kTake, false>(base, kKvTile);
+    } else {
+      for (int ti = 0; ti < n; ++ti) {
+        const int lim = (ok >> ti) & 1 ? len - key0 - ti * kKvTile : 0;  // rows of the sequence
+        uint8_t* tile = base + ti * Gm::kTile;
+        if (lim < kKvTile) blank(tile, lim);
+        tiles<1, true>(tile, lim);
+      }
+    }
+  }
+
+  // kTake tiles from `base` on; with EDGE rows from `lim` on are left out
+  template <int kTake, bool EDGE>
+  __device__ __forceinline__ void tiles(const uint8_t* base, int lim) {
     const int r = g ^ ((g >> 1) & 1);  // row order that spreads the value rows over the banks
     float S[kTake][NT][4];
     float mx[NT][2];
@@ -322,10 +364,8 @@ struct AdWarp {
     for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
     for (int ti = 0; ti < kTake; ++ti) {
-      if (ti < n) {
-        uint8_t* tile = base + ti * Gm::kTile;
-        const int lim = (ok >> ti) & 1 ? len - key0 - ti * kKvTile : 0;  // rows of the sequence
-        if (lim < kKvTile) blank(tile, lim);
+      {
+        const uint8_t* tile = base + ti * Gm::kTile;
         uint32_t w0[2 * NG], w1[2 * NG], a0[NG], a1[NG];
         load_words<2 * NG>(w0, tile + r * Kv::kRow + t * (8 * NG));
         load_words<2 * NG>(w1, tile + (r + 8) * Kv::kRow + t * (8 * NG));
@@ -351,7 +391,7 @@ struct AdWarp {
               }
             }
           }
-        const float in0 = r < lim ? 0.f : -INFINITY, in1 = r + 8 < lim ? 0.f : -INFINITY;
+        const float in0 = !EDGE || r < lim ? 0.f : -INFINITY, in1 = !EDGE || r + 8 < lim ? 0.f : -INFINITY;
         float c0[NG], c1[NG], d0[NG], d1[NG];
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
@@ -413,7 +453,7 @@ struct AdWarp {
     }
 #pragma unroll
     for (int ti = 0; ti < kTake; ++ti) {
-      if (ti < n) {
+      {
         const uint8_t* tile = base + ti * Gm::kTile;
         uint32_t b0[NG], b1[NG];
         load_words<NG>(b0, tile + Kv::kOffVs + r * (4 * NG));
@@ -567,14 +607,14 @@ struct AdWarp {
   // The parts of the pair that warp v ended, or began without ending, joined with those of the
   // warps before it; whether the pair began in this block.
   __device__ __forceinline__ const float* part_of(int v, bool tail) const {
-    const float* own = reinterpret_cast<const float*>(reinterpret_cast<uint8_t*>(info) - Gm::kInfo + v * Gm::kWarp);
+    const float* own = reinterpret_cast<const float*>(reinterpret_cast<uint8_t*>(all) - Gm::kControl + v * Gm::kWarp);
     return tail ? own : own + Gm::kRing / 4;
   }
   __device__ __forceinline__ bool join(int v, bool tail) {
     get(part_of(v, tail));
     while (!tail && --v >= 0) {
-      tail = info[v].tail;
-      if (tail || (info[v].head && !info[v].head_ends)) add(part_of(v, tail));
+      tail = all[v].info.tail;
+      if (tail || (all[v].info.head && !all[v].info.head_ends)) add(part_of(v, tail));
     }
     return tail;
   }
@@ -633,118 +673,168 @@ __global__ void __launch_bounds__(kAdThreads, AdGeom<D, NT>::kBlocks) attn_decod
   grid_launch_dependents();
   grid_dependency_wait();
 
-  // sequences without keys, and lengths beyond their table
-  for (int s = blockIdx.x; s < p.seqs; s += gridDim.x) {
-    if (static_cast<long long>(__ldg(p.lens + s)) > static_cast<long long>(p.width) * p.page_tokens && threadIdx.x == 0)
-      kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
-    if (ad_len(p, s) == 0)
-      for (int i = threadIdx.x; i < p.q_heads * (D / 8); i += kAdThreads)
-        reinterpret_cast<uint4*>(p.out + static_cast<long long>(s) * p.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-
-  // the warp's range of the line
-  auto cost = [&](int len) { return len > 0 ? (len + kKvTile - 1) / kKvTile + kAdPairCost : 0; };
-  long long total = 0;
-  for (int s = lane; s < p.seqs; s += 32) total += cost(ad_len(p, s));
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-  total *= W.hbs;
-  const long long warps = min(static_cast<long long>(gridDim.x) * kAdWarps, total);
+  // the warp's range of the line: `share` places, one more for the first `extra` warps
   const long long me = static_cast<long long>(blockIdx.x) * kAdWarps + W.warp;
-  AdInfo mine{};
+  if (lane == 0) W.my->info = AdInfo{};
   if (threadIdx.x == 0) p.rec[blockIdx.x].first = -1;
-  if (me < warps) {
-    AdCursor cur;
-    cur.x = total * me / warps;
-    cur.end = total * (me + 1) / warps;
-    long long base = 0;  // the line before the sequences of this round
-    for (int s0 = 0;; s0 += 32) {
-      const int len = s0 + lane < p.seqs ? ad_len(p, s0 + lane) : 0;
-      const long long own = static_cast<long long>(cost(len)) * W.hbs;
-      long long upto = own;
+  bool some;
+  {
+    auto cost = [&](int len) { return len > 0 ? (len + kKvTile - 1) / kKvTile + kAdPairCost : 0; };
+    // a lane holds four sequences in a row (all of up to 128, else the sums of its rounds)
+    int len[4];
+    auto take = [&](int s0) {
+      long long sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = s0 + 4 * lane + i;
+        len[i] = s < p.seqs ? ad_len(p, s) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += cost(len[i]);
+      return sum;
+    };
+    auto scan = [&](long long v) {
 #pragma unroll
       for (int x = 1; x < 32; x *= 2) {
-        const long long y = __shfl_up_sync(0xffffffffu, upto, x);
-        if (lane >= x) upto += y;
+        const long long y = __shfl_up_sync(0xffffffffu, v, x);
+        if (lane >= x) v += y;
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, base + upto > cur.x);
-      if (past != 0) {
-        const int who = __ffs(past) - 1;
-        const long long from = base + __shfl_sync(0xffffffffu, upto - own, who);
-        cur.seq = s0 + who;
-        cur.len = __shfl_sync(0xffffffffu, len, who);
-        cur.tiles = (cur.len + kKvTile - 1) / kKvTile;
-        cur.hb = static_cast<int>((cur.x - from) / (cur.tiles + kAdPairCost));
-        cur.pair_x = from + static_cast<long long>(cur.hb) * (cur.tiles + kAdPairCost);
-        break;
+      return v;
+    };
+    long long upto = take(0);
+    for (int s0 = 128; s0 < p.seqs; s0 += 128) upto += take(s0);
+    upto = scan(upto);
+    const long long total = __shfl_sync(0xffffffffu, upto, 31) * W.hbs;
+    const long long warps = min(static_cast<long long>(gridDim.x) * kAdWarps, total);
+    some = me < warps;
+    if (some) {
+      const long long share = div64(total, warps), extra = total - share * warps;
+      const long long x0 = me * share + min(me, extra);
+      long long base = 0;  // the line before the sequences of this round
+      for (int s0 = 0;; s0 += 128) {
+        if (p.seqs > 128) upto = scan(take(s0));
+        const uint32_t past = __ballot_sync(0xffffffffu, (base + upto) * W.hbs > x0);
+        if (past != 0) {
+          if (lane == __ffs(past) - 1) {
+            AdControl& c = *W.my;
+            long long from = base + upto;
+            int at = 3;
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+              if (from * W.hbs > x0) {
+                from -= cost(len[i]);
+                at = i;
+              }
+            }
+            from *= W.hbs;
+            int own = len[0];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) own = at == i ? len[i] : own;
+            c.x = x0;
+            c.end = x0 + share + (me < extra ? 1 : 0);
+            c.seq = s0 + 4 * lane + at;
+            c.len = own;
+            c.tiles = (own + kKvTile - 1) / kKvTile;
+            c.hb = static_cast<int>(div64(x0 - from, c.tiles + kAdPairCost));
+            c.pair_x = from + static_cast<long long>(c.hb) * (c.tiles + kAdPairCost);
+            c.share = share;
+            c.extra = extra;
+          }
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
       }
-      base += __shfl_sync(0xffffffffu, upto, 31);
     }
+  }
+  // sequences without keys, and lengths beyond their table
+  auto rest = [&]() {
+    for (int s = blockIdx.x; s < p.seqs; s += gridDim.x) {
+      if (static_cast<long long>(__ldg(p.lens + s)) > static_cast<long long>(p.width) * p.page_tokens && threadIdx.x == 0)
+        kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
+      if (ad_len(p, s) == 0)
+        for (int i = threadIdx.x; i < p.q_heads * (D / 8); i += kAdThreads)
+          reinterpret_cast<uint4*>(p.out + static_cast<long long>(s) * p.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  if (!some) rest();
+  if (some) {
+    __syncwarp();
 
     // copies run up to kStages steps ahead of the arithmetic, over the ends of parts too
-    AdCursor ahead = cur;
-    AdPart fr{};
-    int flo = 0;
-    bool more = true;
-    uint32_t issued = 0, done = 0, oks = 0;  // oks: 4 bits per ring slot
+    int flo = 0, fend = 0, fkvh = 0;
+    uint32_t pushed = 0;                     // parts
+    uint32_t issued = 0, done = 0, oks = 0;  // copies; 4 bits per ring slot
     auto refill = [&]() {
-      while (more && issued - done < Gm::kStages) {
-        if (flo >= fr.b) {
-          if (!W.next(ahead, fr)) {
-            more = false;
-            return;
-          }
-          flo = fr.a;
+      while (issued - done < Gm::kStages) {
+        const bool first = flo >= fend;
+        if (first) {
+          if (!W.next(pushed % kAdParts)) return;
+          const AdPart& r = W.my->part[pushed++ % kAdParts];
+          flo = r.a;
+          fend = r.b;
+          fkvh = r.kvh;
         }
         const uint32_t slot = issued % Gm::kStages;
-        const int n = min(Gm::kTake, fr.b - flo);
-        oks = (oks & ~(0xFu << (4 * slot))) | (W.fetch(fr, flo, n, slot) << (4 * slot));
+        const int n = min(Gm::kTake, fend - flo);
+        oks = (oks & ~(0xFu << (4 * slot))) |
+              (W.fetch(W.my->part[(pushed - 1) % kAdParts], fkvh, first, flo, n, slot) << (4 * slot));
         flo += n;
         ++issued;
       }
     };
     refill();
-    AdPart r;
-    while (W.next(cur, r)) {
+    rest();  // while the first copies are on their way
+    for (uint32_t at = 0; at < pushed; ++at) {
+      const AdPart& r = W.my->part[at % kAdParts];
       W.start(r.seq, r.kvh, r.hb - r.kvh * p.qblocks);
-      for (int lo = r.a; lo < r.b; lo += Gm::kTake) {
+      const int end = r.b, len = r.len;
+      for (int lo = r.a; lo < end; lo += Gm::kTake) {
         const uint32_t slot = done % Gm::kStages;
         W.wait(slot, (done / Gm::kStages) & 1u);
-        W.step(slot, min(Gm::kTake, r.b - lo), (oks >> (4 * slot)) & 0xFu, lo * kKvTile, r.len);
+        W.step(slot, min(Gm::kTake, end - lo), (oks >> (4 * slot)) & 0xFu, lo * kKvTile, len);
         __syncwarp();
         ++done;
         refill();
       }
       W.finish();
-      mine.some = 1;
       if (r.a > 0) {
         W.put(W.head);
-        mine.head = 1;
-        mine.head_ends = r.b == r.tiles;
-        mine.seq = r.seq;
-        mine.hb = r.hb;
-        mine.pair_x = r.pair_x;
-      } else if (r.b < r.tiles) {
+      } else if (end < r.tiles) {
         W.put(reinterpret_cast<float*>(W.ring));  // the range ends here: its copies are read
-        mine.tail = 1;
       } else {
         W.write_out(r.seq, r.hb);
       }
+      if (lane == 0) {
+        AdInfo& mine = W.my->info;
+        mine.some = 1;
+        if (r.a > 0) {
+          mine.head = 1;
+          mine.head_ends = end == r.tiles;
+          mine.seq = r.seq;
+          mine.hb = r.hb;
+          mine.pair_x = r.pair_x;
+        } else if (end < r.tiles) {
+          mine.tail = 1;
+        }
+      }
     }
   }
-  if (lane == 0) W.info[W.warp] = mine;
   __syncthreads();
   // pairs that end in this warp and began before it
+  const AdInfo& mine = W.my->info;
   if (mine.head && mine.head_ends) {
     if (W.join(W.warp, false)) {
       W.write_out(mine.seq, mine.hb);
     } else {
       W.write_part(0);
       if (lane == 0) {
-        // the place u of the line lies in the range of warp ((u + 1) warps - 1) / total
+        // the warp whose range holds the pair's first tile
         const int kvh = mine.hb / p.qblocks, q0 = (mine.hb - kvh * p.qblocks) * 8 * NT;
+        const long long u = mine.pair_x + kAdPairCost, share = W.my->share, extra = W.my->extra;
+        const long long more = extra * (share + 1);
+        const long long w = u < more ? div64(u, share + 1) : extra + div64(u - more, share);
         AdRecord rec;
-        rec.first = static_cast<int>(((mine.pair_x + kAdPairCost + 1) * warps - 1) / total) / kAdWarps;
+        rec.first = static_cast<int>(w) / kAdWarps;
         rec.seq = mine.seq;
         rec.head0 = kvh * p.group + q0;
         rec.queries = min(8 * NT, p.group - q0);
@@ -755,8 +845,8 @@ __global__ void __launch_bounds__(kAdThreads, AdGeom<D, NT>::kBlocks) attn_decod
   // the pair that goes on behind the block
   if (W.warp == kAdWarps - 1) {
     int v = W.warp;
-    while (v > 0 && !W.info[v].some) --v;
-    const AdInfo& last = W.info[v];
+    while (v > 0 && !W.all[v].info.some) --v;
+    const AdInfo& last = W.all[v].info;
     if (last.tail || (last.head && !last.head_ends)) {
       W.join(v, last.tail);
       W.write_part(1);
@@ -764,61 +854,145 @@ __global__ void __launch_bounds__(kAdThreads, AdGeom<D, NT>::kBlocks) attn_decod
   }
 }
 
-// Joins the parts of a pair that blocks first .. b hold: block (b, query).  Warps take every
-// eighth part, a lane 4 (D = 64: 2) channels.
-constexpr int kAjWarps = 8;
+// Joins the parts of pairs that lie in several blocks.  Every block finds the records of such
+// pairs; a (pair, query) with few parts is one warp's work, one with many (a long context: all
+// blocks of the line hold parts) a whole block's, so that its parts are in flight together.
+constexpr int kAjWarps = 16;
+constexpr int kAjFew = 8;  // blocks behind a pair's first from which on it has many parts
 template <int D, int NT>
 __global__ void __launch_bounds__(kAjWarps * 32) attn_join_kernel(const __grid_constant__ AdParams p) {
   constexpr int C = D / 32;
-  __shared__ float sl[kAjWarps], so[kAjWarps][D];
+  __shared__ AdRecord recs[kAdMaxBlocks];
+  __shared__ int at[kAdMaxBlocks];
+  __shared__ int2 count[kAjWarps];
+  __shared__ float sm[kAjWarps], sl[kAjWarps], so[kAjWarps][D];
   grid_dependency_wait();
   grid_launch_dependents();
-  const AdRecord r = p.rec[blockIdx.x];
-  const int qi = blockIdx.y;
-  if (r.first < 0 || qi >= r.queries) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int last = blockIdx.x;
-  auto row = [&](int b) { return (static_cast<long long>(b) * 2 + (b == last ? 0 : 1)) * (8 * NT) + qi; };
-  // the largest reference, then the weighted sums
-  float m = -INFINITY;
-  for (int b = r.first + lane; b <= last; b += 32) m = fmaxf(m, p.part_ml[2 * row(b)]);
+  // records of pairs with few parts from the front, with many from the back, in their blocks' order
+  int few = 0, many = 0;
+  for (int b0 = 0; b0 < p.blocks; b0 += kAjWarps * 32) {
+    const int b = b0 + threadIdx.x;
+    AdRecord r;
+    r.first = -1;
+    if (b < p.blocks) r = p.rec[b];
+    const bool is_many = r.first >= 0 && b - r.first >= kAjFew, is_few = r.first >= 0 && !is_many;
+    const uint32_t got_few = __ballot_sync(0xffffffffu, is_few), got_many = __ballot_sync(0xffffffffu, is_many);
+    if (lane == 0) count[warp] = make_int2(__popc(got_few), __popc(got_many));
+    __syncthreads();
+    int i = few + __popc(got_few & ((1u << lane) - 1)), j = many + __popc(got_many & ((1u << lane) - 1));
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) o[c] = 0.f;
-#pragma unroll 8
-  for (int b = r.first + warp; b <= last; b += kAjWarps) {
-    const long long at = row(b);
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-    float v[C];
-    if constexpr (C == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p.part + at * D + 4 * lane);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(p.part + at * D + 2 * lane);
-      v[0] = x.x, v[1] = x.y;
+    for (int w = 0; w < kAjWarps; ++w) {
+      const int2 c = count[w];
+      if (w < warp) {
+        i += c.x;
+        j += c.y;
+      }
+      few += c.x;
+      many += c.y;
     }
-    const float w = ex2(ml.x - ref);
-    l = fmaf(w, ml.y, l);
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = fmaf(w, v[c], o[c]);
+    if (is_many) i = kAdMaxBlocks - 1 - j;
+    if (r.first >= 0) {
+      recs[i] = r;
+      at[i] = b;
+    }
+    __syncthreads();
   }
+
+  // parts `from`, from + step, .. of record i and query qi: their sums relative to their largest reference
+  struct Sums {
+    float m, l, o[C];
+  };
+  auto gather = [&](auto round, int i, int qi, int from, int step) {
+    constexpr int kRound = decltype(round)::value;  // loads in flight
+    const int last = at[i];
+    Sums s;
+    s.m = -INFINITY;
+    s.l = 0.f;
 #pragma unroll
-  for (int c = 0; c < C; ++c) so[warp][C * lane + c] = o[c];
-  if (lane == 0) sl[warp] = l;
-  __syncthreads();
-  const int ch = threadIdx.x;
-  if (ch >= D) return;
-  float L = 0.f, v = 0.f;
+    for (int c = 0; c < C; ++c) s.o[c] = 0.f;
+    for (int b0 = recs[i].first + from; b0 <= last; b0 += kRound * step) {
+      float2 ml[kRound];
+      float v[kRound][C];
 #pragma unroll
-  for (int w = 0; w < kAjWarps; ++w) {
-    L += sl[w];
-    v += so[w][ch];
+      for (int k = 0; k < kRound; ++k) {
+        const int b = b0 + k * step;
+        ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[k][c] = 0.f;
+        if (b <= last) {
+          const long long row = (static_cast<long long>(b) * 2 + (b == last ? 0 : 1)) * (8 * NT) + qi;
+          ml[k] = *reinterpret_cast<const float2*>(p.part_ml + 2 * row);
+          if constexpr (C == 4)
+            *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(p.part + row * D + 4 * lane);
+          else
+            *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(p.part + row * D + 2 * lane);
+        }
+      }
+      float m = s.m;
+#pragma unroll
+      for (int k = 0; k < kRound; ++k) m = fmaxf(m, ml[k].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float old = ex2(s.m - ref);
+      s.m = m;
+      s.l *= old;
+#pragma unroll
+      for (int c = 0; c < C; ++c) s.o[c] *= old;
+#pragma unroll
+      for (int k = 0; k < kRound; ++k) {
+        const float w = ex2(ml[k].x - ref);
+        s.l = fmaf(w, ml[k].y, s.l);
+#pragma unroll
+        for (int c = 0; c < C; ++c) s.o[c] = fmaf(w, v[k][c], s.o[c]);
+      }
+    }
+    return s;
+  };
+  auto write = [&](int i, int qi, const float (&o)[C], float l) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* dst = p.out + (static_cast<long long>(recs[i].seq) * p.q_heads + recs[i].head0 + qi) * D + C * lane;
+    if constexpr (C == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[0] * inv, o[1] * inv);
+  };
+
+  const int queries = min(8 * NT, p.group);
+  for (int it = blockIdx.x * kAjWarps + warp; it < few * queries; it += gridDim.x * kAjWarps) {
+    const int i = it / queries, qi = it - i * queries;
+    if (qi >= recs[i].queries) continue;
+    const Sums s = gather(std::integral_constant<int, 4>(), i, qi, 0, 1);
+    write(i, qi, s.o, s.l);
   }
-  const __nv_bfloat16 y = __float2bfloat16_rn(L == 0.f ? 0.f : v * (1.f / L));
-  p.out[(static_cast<long long>(r.seq) * p.q_heads + r.head0 + qi) * D + ch] = *reinterpret_cast<const uint16_t*>(&y);
+  for (int it = blockIdx.x; it < many * queries; it += gridDim.x) {  // the same for all of the block
+    const int j = it / queries, qi = it - j * queries, i = kAdMaxBlocks - 1 - j;
+    if (qi >= recs[i].queries) continue;
+    const Sums s = gather(std::integral_constant<int, 10>(), i, qi, warp, kAjWarps);
+    if (lane == 0) {
+      sm[warp] = s.m;
+      sl[warp] = s.l;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) so[warp][C * lane + c] = s.o[c];
+    __syncthreads();
+    if (warp == 0) {
+      float m = -INFINITY, l = 0.f, o[C];
+#pragma unroll
+      for (int w = 0; w < kAjWarps; ++w) m = fmaxf(m, sm[w]);
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAjWarps; ++w) {
+        const float f = ex2(sm[w] - ref);
+        l = fmaf(f, sl[w], l);
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = fmaf(f, so[w][C * lane + c], o[c]);
+      }
+      write(i, qi, o, l);
+    }
+    __syncthreads();
+  }
 }
 
 }  // namespace fmoe
