@@ -55,6 +55,15 @@ def lib():
     return _lib
 
 
+def _stream(stream, t) -> int:
+    """The raw stream handle to launch on; the tensors' device has to be the current one.
+    (torch.cuda.current_stream() takes 3 us, as long as a small call's launch.)"""
+    d = t.get_device()
+    if d != torch._C._cuda_getDevice():
+        _refuse(f"the tensors are on device {d}, which is not the current one")
+    return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+
+
 def _refuse(what: str):
     raise fmoe.FmoeError(1, what)
 
@@ -156,7 +165,7 @@ def fmoe_kv_append(cfg: fmoe_attn_config, q, k, v, rope, positions, slots, cache
     cp, pages = _pages(cfg, cache)
     st = lib().fmoe_kv_append(cfg.ref, qp, qs, kp, ks, vp, vs, T, table, known, rotary, pos,
                               _ints(slots, torch.int64, (T,), "slots"), cp, pages, qo, ko, _error(error),
-                              fmoe._stream(stream))
+                              _stream(stream, cache))
     fmoe._check(st, "fmoe_kv_append")
 
 
@@ -172,7 +181,7 @@ def fmoe_kv_gather(cfg: fmoe_attn_config, cache, page_table, cu, k_out, v_out, f
     cp, pages = _pages(cfg, cache)
     st = lib().fmoe_kv_gather(cfg.ref, cp, pages, _ints(page_table, torch.int32, (seqs, width), "page_table"), width, seqs,
                               None if first is None else _ints(first, torch.int32, (seqs,), "first"),
-                              _ints(cu, torch.int32, (seqs + 1,), "cu"), n, kp, vp, _error(error), fmoe._stream(stream))
+                              _ints(cu, torch.int32, (seqs + 1,), "cu"), n, kp, vp, _error(error), _stream(stream, cache))
     fmoe._check(st, "fmoe_kv_gather")
 
 
@@ -188,7 +197,7 @@ def fmoe_attn_decode(cfg: fmoe_attn_config, q, cache, page_table, lens, out, sca
     cp, pages = _pages(cfg, cache)
     st = lib().fmoe_attn_decode(cfg.ref, qp, qs, cp, pages, _ints(page_table, torch.int32, (seqs, width), "page_table"),
                                 width, _ints(lens, torch.int32, (seqs,), "lens"), seqs, scale, op, workspace.data_ptr(),
-                                workspace.numel(), _error(error), fmoe._stream(stream))
+                                workspace.numel(), _error(error), _stream(stream, q))
     fmoe._check(st, "fmoe_attn_decode")
     return out
 
@@ -206,6 +215,6 @@ def fmoe_attn_prompt(cfg: fmoe_attn_config, q, k, v, cu_q, cu_k, out, scale, err
         _refuse("k and v, and q and out, have as many rows as each other")
     st = lib().fmoe_attn_prompt(cfg.ref, qp, qs, kp, ks, vp, vs, _ints(cu_q, torch.int32, (seqs + 1,), "cu_q"),
                                 _ints(cu_k, torch.int32, (seqs + 1,), "cu_k"), seqs, n, m, scale, op, _error(error),
-                                fmoe._stream(stream))
+                                _stream(stream, q))
     fmoe._check(st, "fmoe_attn_prompt")
     return out

@@ -15,6 +15,8 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int kMaxGridY = 65535;
+constexpr int kFewTokens = 480;  // fmoe_kv_append: 300 tokens of 32 + 2 x 4 heads take 6.3 us by blocks, 8.1 by warps; 600: 9.8, 8.5
+constexpr int kGatherWide = 400;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 5.5 us 64 rows a block, 4.8 us 16; 4000: 6.9, 7.6
 
 bool on_boundary(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -111,6 +113,14 @@ fmoe_status decode(AdParams& p, int sms, int device, int64_t places, void* strea
                      : launch(attn_join_kernel<D, NT>, dim3((unsigned)(items < sms ? items : sms)), kAjWarps * 32, 0, stream, p);
 }
 
+// 64 rows per block where that makes blocks enough for the device, else 16.
+template <int D>
+fmoe_status gather(const KvGatherParams& p, int64_t rows, void* stream) {
+  const dim3 wide((unsigned)((rows + 63) / 64), (unsigned)p.kv_heads), narrow((unsigned)((rows + 15) / 16), (unsigned)p.kv_heads);
+  return (rows + 63) / 64 * p.kv_heads >= kGatherWide ? launch(kv_gather_kernel<D, 64>, wide, kKvThreads, 0, stream, p)
+                                              : launch(kv_gather_kernel<D, 16>, narrow, kKvThreads, 0, stream, p);
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -183,11 +193,18 @@ fmoe_status fmoe_kv_append(const fmoe_attn_config* c, const uint16_t* q, int64_t
   p.q_out = q_out, p.k_out = k_out, p.err = device_error;
   p.rope_positions = rope_positions, p.rotary = rotary;
   p.q_heads = c->q_heads, p.kv_heads = c->kv_heads, p.page_tokens = c->page_tokens;
-  // few tokens: their heads over more blocks, one head row per lane group
+  // few tokens: one per block, their heads over several blocks, one per lane group;
+  // many: one per warp
   const int per = kKvThreads / (D / 8), heads = (q ? c->q_heads : 0) + 2 * c->kv_heads;
-  int y = T < 512 ? (heads + per - 1) / per : 1;
+  p.tokens = T;
+  const bool few = T < kFewTokens;
+  const int groups = few ? per : 32 / (D / 8);
+  int y = few ? (heads + per - 1) / per : 1;
   if (y > kMaxGridY) y = kMaxGridY;
-  const dim3 grid((unsigned)T, (unsigned)y);
+  p.groups_log2 = __builtin_ctz(groups);
+  p.kv_turn = (groups * y - (q ? c->q_heads : 0) % (groups * y)) % (groups * y);
+  const int together = per / groups;
+  const dim3 grid((unsigned)((T + together - 1) / together), (unsigned)y);
   return D == 128 ? launch(kv_append_kernel<128>, grid, kKvThreads, 0, stream, p)
                   : launch(kv_append_kernel<64>, grid, kKvThreads, 0, stream, p);
 }
@@ -209,9 +226,7 @@ fmoe_status fmoe_kv_gather(const fmoe_attn_config* c, const void* cache, int64_t
   p.table = page_table, p.first = first, p.cu = cu;
   p.k_out = k_out, p.v_out = v_out, p.err = device_error;
   p.width = table_width, p.seqs = seqs, p.kv_heads = c->kv_heads, p.page_tokens = c->page_tokens;
-  const dim3 grid((unsigned)((rows + kKvGatherRows - 1) / kKvGatherRows), (unsigned)c->kv_heads);
-  return c->head_dim == 128 ? launch(kv_gather_kernel<128>, grid, kKvThreads, 0, stream, p)
-                            : launch(kv_gather_kernel<64>, grid, kKvThreads, 0, stream, p);
+  return c->head_dim == 128 ? gather<128>(p, rows, stream) : gather<64>(p, rows, stream);
 }
 
 fmoe_status fmoe_attn_decode(const fmoe_attn_config* c, const uint16_t* q, int64_t q_stride, const void* cache,

@@ -101,12 +101,6 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w8, int i) {
   return (i < 2 ? w : w8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
 
-// Quotient of numbers that are hardly ever past 32 bits.
-__device__ __forceinline__ long long div64(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
 __device__ __forceinline__ int ad_len(const AdParams& p, int s) {
   const int len = __ldg(p.lens + s);
   const long long most = static_cast<long long>(p.width) * p.page_tokens;

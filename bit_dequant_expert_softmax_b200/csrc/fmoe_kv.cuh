@@ -23,6 +23,7 @@ namespace fmoe {
 
 constexpr int kKvTile = 16;      // tokens of a cache tile
 constexpr int kKvThreads = 256;
+constexpr int kKvAhead = 2;      // head rows of a lane group in flight
 
 template <int D>
 struct KvGeom {
@@ -51,6 +52,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Quotient of numbers that are hardly ever past 32 bits.
+__device__ __forceinline__ long long div64(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 struct KvAppendParams {
   const uint16_t *q, *k, *v;
   long long q_stride, k_stride, v_stride;
@@ -61,120 +68,169 @@ struct KvAppendParams {
   long long pages, page_bytes;
   uint16_t *q_out, *k_out;
   uint32_t* err;
+  int tokens, groups_log2, kv_turn;  // kv_turn: key/value heads start where the query heads end
   int rope_positions, rotary, q_heads, kv_heads, page_tokens;
 };
 
-// One token per block (blockIdx.x), its heads (queries, keys, values in this order) over
-// the block's lane groups and blockIdx.y.  A lane owns 8 channels of a head row, which is
-// one code word; a group's minimum and maximum are reduced over its 8 lanes.  The token's
-// cosines and sines of the lane's channels are loaded once for all of its heads.
+// Codes, scale and bias of a 64-channel group whose 8 lanes (of `mask`) hold 8 channels each:
+// this lane's code word, and the group's (scale, bias) word.
+__device__ __forceinline__ uint2 kv_quantise(const uint32_t (&w)[4], uint32_t mask) {
+  float lo = bf16_lo(w[0]), hi = lo;
+  uint32_t odd = 0;  // an infinity or a NaN
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo = fminf(lo, fminf(bf16_lo(w[i]), bf16_hi(w[i])));
+    hi = fmaxf(hi, fmaxf(bf16_lo(w[i]), bf16_hi(w[i])));
+    odd |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+  }
+#pragma unroll
+  for (int off = 1; off < 8; off *= 2) {
+    lo = fminf(lo, __shfl_xor_sync(mask, lo, off));
+    hi = fmaxf(hi, __shfl_xor_sync(mask, hi, off));
+    odd |= __shfl_xor_sync(mask, odd, off);
+  }
+  if (odd) return make_uint2(0u, 0x7FC00000u);
+  // halves: max - min of finite bf16 may pass the largest float, their halves' cannot
+  const float lo2 = 0.5f * lo;
+  const float s = bf16_lo(pack_bf16(__fdiv_rn(__fsub_rn(0.5f * hi, lo2), 7.5f), 0.f));
+  uint32_t code = 0;
+  if (s > 0.f) {
+    // rint of the rounded quotient x / y by a product with 1/y (off by under 3e-6 below 16); a
+    // result that near to a tie is decided by the remainder, or by the quotient itself
+    // (tiny groups are scaled up, exactly: 1/y stays finite)
+    const float k = s < 0x1p-60f ? 0x1p65f : 0.5f, y = k * s, inv = __frcp_rn(y), base = k * lo;
+    constexpr float kMagic = 12582912.f;  // 1.5 2^23: the sum's low bits are the rounded number
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      const float x = __fsub_rn(k * (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])), base);
+      const float q = fminf(x * inv, 15.f);
+      float t = q + kMagic;
+      if (fabsf(q - (t - kMagic)) > 0.499996f) {
+        const float h = truncf(q) + 0.5f;
+        t = rintf(fmaf(-h, y, x) == 0.f ? h : fminf(__fdiv_rn(x, y), 15.f)) + kMagic;
+      }
+      code = code * 16u + (__float_as_uint(t) - __float_as_uint(kMagic));
+    }
+  }
+  return make_uint2(code, (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u));
+}
+
+// 2^groups_log2 of a block's lane groups take one token, whose heads they and blockIdx.y share out
+// (the query heads, then the key/value heads): all groups of a block and several blocks when
+// there are few tokens, one warp's when there are many, so that every warp has its own chain of
+// loads.  A lane owns 8 channels of a head row, which is one code word; a group's minimum and
+// maximum are reduced over its 8 lanes.  The token's cosines and sines of the lane's channels are
+// loaded once for all of its heads, and the first rows before the slot and position are looked at.
 template <int D>
 __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   using Gm = KvGeom<D>;
-  constexpr int kPer = kKvThreads / Gm::kLanes;  // head rows in flight per block
+  constexpr int kPer = kKvThreads / Gm::kLanes;  // lane groups of a block
   grid_launch_dependents();
   grid_dependency_wait();
-  const long long tok = blockIdx.x;
+  const int lane = threadIdx.x % Gm::kLanes, grp = threadIdx.x / Gm::kLanes, in = grp & ((1 << p.groups_log2) - 1);
+  const uint32_t mask = ((1u << Gm::kLanes) - 1) << (threadIdx.x & 31 & ~(Gm::kLanes - 1));  // the lane group
+  const long long tok = static_cast<long long>(blockIdx.x) * (kPer >> p.groups_log2) + (grp >> p.groups_log2);
+  if (tok >= p.tokens) return;
+  const int half = p.rotary / 2, c0 = lane * 8;
+  const bool turned = c0 < p.rotary, first = c0 < half;
+  const int step = gridDim.y << p.groups_log2, id = (blockIdx.y << p.groups_log2) + in;
+  const int q_heads = p.q != nullptr ? p.q_heads : 0;
+  const int pair = (first ? c0 + half : c0 - half) / 8;  // the lane with the other channels of the rotated pairs
+  const uint16_t* q = p.q + tok * p.q_stride + c0;
+  const uint16_t* k = p.k + tok * p.k_stride + c0;
+  const uint16_t* v = p.v + tok * p.v_stride + c0;
+  auto row_of = [](const uint16_t* src, bool is) { return is ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u); };
+
   const long long slot = __ldg(p.slots + tok);
+  const int pos = p.rotary > 0 ? __ldg(p.positions + tok) : 0;
+  int h = id, hk = id + p.kv_turn - (id + p.kv_turn >= step ? step : 0);  // behind the query heads
+  uint4 next_q[kKvAhead], next_kv;
+  auto load_q = [&]() {
+#pragma unroll
+    for (int u = 0; u < kKvAhead; ++u) next_q[u] = row_of(q + (h + u * step) * D, h + u * step < q_heads);
+  };
+  auto load_kv = [&]() {  // key heads, then value heads
+    next_kv = row_of(hk < p.kv_heads ? k + hk * D : v + (hk - p.kv_heads) * D, hk < 2 * p.kv_heads);
+  };
+  load_q();
+  load_kv();
+
+  const bool speaks = lane == 0 && id == 0;
   if (slot < 0) return;
-  const long long page = slot / p.page_tokens;
+  const long long page = div64(slot, p.page_tokens);
   if (page >= p.pages) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) kv_error(p.err, FMOE_DEVERR_BAD_SLOT);
+    if (speaks) kv_error(p.err, FMOE_DEVERR_BAD_SLOT);
     return;
   }
   const int place = static_cast<int>(slot - page * p.page_tokens);
-  const int lane = threadIdx.x % Gm::kLanes, grp = threadIdx.x / Gm::kLanes;
-  const int half = p.rotary / 2, c0 = lane * 8;
-  const bool turned = c0 < p.rotary, first = c0 < half;
   float cs[8], sn[8];
   if (p.rotary > 0) {
-    const int pos = __ldg(p.positions + tok);
     if (pos < 0 || pos >= p.rope_positions) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) kv_error(p.err, FMOE_DEVERR_BAD_POSITION);
+      if (speaks) kv_error(p.err, FMOE_DEVERR_BAD_POSITION);
       return;
     }
     if (turned) {
-      const float4* row = reinterpret_cast<const float4*>(p.rope + static_cast<long long>(pos) * p.rotary +
-                                                          (first ? c0 : c0 - half));
-      const float4 a = __ldg(row), b = __ldg(row + 1);
-      const float4 c = __ldg(row + half / 4), d = __ldg(row + half / 4 + 1);
+      const float4* at = reinterpret_cast<const float4*>(p.rope + static_cast<long long>(pos) * p.rotary + (first ? c0 : c0 - half));
+      const float4 a = __ldg(at), b = __ldg(at + 1), c = __ldg(at + half / 4), d = __ldg(at + half / 4 + 1);
       cs[0] = a.x, cs[1] = a.y, cs[2] = a.z, cs[3] = a.w, cs[4] = b.x, cs[5] = b.y, cs[6] = b.z, cs[7] = b.w;
       sn[0] = c.x, sn[1] = c.y, sn[2] = c.z, sn[3] = c.w, sn[4] = d.x, sn[5] = d.y, sn[6] = d.z, sn[7] = d.w;
+      if (first) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sn[i] = -sn[i];  // y_i = x_i c - x_{i+R/2} s
+      }
     }
   }
+  // A row's partners come from the lanes that hold them (so that a row may be rotated in
+  // place).  Products and sums are rounded one by one: the result does not depend on which half
+  // of the pair a lane holds.
+  auto rotate = [&](uint32_t (&w)[4], const uint4& x) {
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    uint32_t z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = __shfl_sync(mask, w[i], pair, Gm::kLanes);
+    if (!turned) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack_bf16(__fadd_rn(__fmul_rn(bf16_lo(w[i]), cs[2 * i]), __fmul_rn(bf16_lo(z[i]), sn[2 * i])),
+                       __fadd_rn(__fmul_rn(bf16_hi(w[i]), cs[2 * i + 1]), __fmul_rn(bf16_hi(z[i]), sn[2 * i + 1])));
+    }
+  };
+
+  uint16_t* q_out = p.q_out + tok * p.q_heads * D + c0;
+  while (h < q_heads) {
+    uint4 x[kKvAhead];
+#pragma unroll
+    for (int u = 0; u < kKvAhead; ++u) x[u] = next_q[u];
+    const int h0 = h;
+    h += kKvAhead * step;
+    load_q();
+#pragma unroll
+    for (int u = 0; u < kKvAhead; ++u) {
+      const int i = h0 + u * step;
+      uint32_t w[4];
+      rotate(w, x[u]);
+      if (i < q_heads) *reinterpret_cast<uint4*>(q_out + i * D) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+
   uint8_t* tile0 = p.cache + page * p.page_bytes + static_cast<long long>(place / kKvTile) * Gm::kTileBytes;
   const long long head_bytes = static_cast<long long>(p.page_tokens / kKvTile) * Gm::kTileBytes;
-  const int row = place % kKvTile, grp64 = lane / 8;
-  const int h_q = p.q != nullptr ? 0 : p.q_heads;
-  const int heads = p.q_heads + 2 * p.kv_heads;
-  for (int h0 = h_q + blockIdx.y * kPer; h0 < heads; h0 += kPer * gridDim.y) {  // uniform over the block
-    const int h = h0 + grp;
-    const bool live = h < heads;
-    const int kind = h < p.q_heads ? 0 : h < p.q_heads + p.kv_heads ? 1 : 2;
-    const int hk = kind == 0 ? h : kind == 1 ? h - p.q_heads : h - p.q_heads - p.kv_heads;
-    const uint16_t* src = (kind == 0 ? p.q + tok * p.q_stride : kind == 1 ? p.k + tok * p.k_stride : p.v + tok * p.v_stride) +
-                          static_cast<long long>(hk) * D;
-    const bool turn = live && turned && kind < 2;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-    if (live) x = *reinterpret_cast<const uint4*>(src + c0);
-    if (turn) y = *reinterpret_cast<const uint4*>(src + (first ? c0 + half : c0 - half));
-    __syncwarp();  // a row rotated in place is read by all of its lanes before any writes
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    if (turn) {
-      const uint32_t z[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // products and sum rounded one by one (no contraction): the result does not
-        // depend on which half of the pair a lane holds
-        const float p0 = __fmul_rn(bf16_lo(z[i]), sn[2 * i]), p1 = __fmul_rn(bf16_hi(z[i]), sn[2 * i + 1]);
-        const float a0 = __fmul_rn(bf16_lo(w[i]), cs[2 * i]), a1 = __fmul_rn(bf16_hi(w[i]), cs[2 * i + 1]);
-        w[i] = first ? pack_bf16(__fsub_rn(a0, p0), __fsub_rn(a1, p1)) : pack_bf16(__fadd_rn(a0, p0), __fadd_rn(a1, p1));
-      }
+  const int row = place % kKvTile, word = (lane & 7) * Gm::kGroups + lane / 8, sb_word = row * Gm::kGroups + lane / 8;
+  while (hk < 2 * p.kv_heads) {
+    const bool key = hk < p.kv_heads;
+    const int i = key ? hk : hk - p.kv_heads;
+    uint32_t w[4] = {next_kv.x, next_kv.y, next_kv.z, next_kv.w};
+    if (key) {
+      rotate(w, next_kv);
+      if (p.k_out != nullptr)
+        *reinterpret_cast<uint4*>(p.k_out + (tok * p.kv_heads + i) * D + c0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    uint16_t* dst = kind == 0 ? p.q_out : kind == 1 ? p.k_out : nullptr;
-    if (live && dst != nullptr)
-      *reinterpret_cast<uint4*>(dst + (tok * (kind == 0 ? p.q_heads : p.kv_heads) + hk) * D + c0) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    // the group's quantisation (query rows go through it too where a warp holds both)
-    if (__any_sync(0xffffffffu, live && kind > 0)) {
-      float lo = bf16_lo(w[0]), hi = lo;
-      uint32_t odd = 0;  // an infinity or a NaN
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo = fminf(lo, fminf(bf16_lo(w[i]), bf16_hi(w[i])));
-        hi = fmaxf(hi, fmaxf(bf16_lo(w[i]), bf16_hi(w[i])));
-        odd |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
-      }
-#pragma unroll
-      for (int off = 1; off < 8; off *= 2) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-        odd |= __shfl_xor_sync(0xffffffffu, odd, off);
-      }
-      // halves: max - min of finite bf16 may pass the largest float, their halves' cannot
-      const float lo2 = 0.5f * lo;
-      const float s = bf16_lo(pack_bf16(__fdiv_rn(__fsub_rn(0.5f * hi, lo2), 7.5f), 0.f));
-      const float s2 = 0.5f * s;
-      uint32_t code = 0;
-      if (odd == 0 && s > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float r0 = rintf(__fdiv_rn(__fsub_rn(0.5f * bf16_lo(w[i]), lo2), s2));
-          const float r1 = rintf(__fdiv_rn(__fsub_rn(0.5f * bf16_hi(w[i]), lo2), s2));
-          code |= static_cast<uint32_t>(fminf(r0, 15.f)) << (8 * i);
-          code |= static_cast<uint32_t>(fminf(r1, 15.f)) << (8 * i + 4);
-        }
-      }
-      if (live && kind > 0) {
-        uint8_t* tile = tile0 + hk * head_bytes;
-        uint8_t* crow = tile + (kind == 2 ? Gm::kOffV : 0) + row * Gm::kRow;
-        reinterpret_cast<uint32_t*>(crow)[(lane & 7) * Gm::kGroups + grp64] = code;
-        if ((lane & 7) == 0) {
-          const uint32_t sb = odd ? 0x7FC00000u : (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
-          reinterpret_cast<uint32_t*>(tile + (kind == 2 ? Gm::kOffVs : Gm::kOffKs))[row * Gm::kGroups + grp64] = sb;
-        }
-      }
-    }
+    uint8_t* tile = tile0 + i * head_bytes;
+    hk += step;
+    load_kv();
+    const uint2 a = kv_quantise(w, mask);
+    reinterpret_cast<uint32_t*>(tile + (key ? 0 : Gm::kOffV) + row * Gm::kRow)[word] = a.x;
+    if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(tile + (key ? Gm::kOffKs : Gm::kOffVs))[sb_word] = a.y;
   }
 }
 
@@ -187,51 +243,55 @@ struct KvGatherParams {
   int width, seqs, kv_heads, page_tokens;
 };
 
-constexpr int kKvGatherRows = 16;  // rows per block
 
-// kKvGatherRows packed rows per block (blockIdx.x), heads over blockIdx.y.  The first
-// threads find each row's place in the cache (-1: none); then a lane group takes one head's
-// keys or values of one row.
-template <int D>
+// `Rows` packed rows per block (blockIdx.x), heads over blockIdx.y.  The first threads find each
+// row's place in the cache (-1: none); then a lane group takes one head's keys or values of one
+// row, up to 8 of them in flight.
+template <int D, int Rows>
 __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const __grid_constant__ KvGatherParams p) {
   using Gm = KvGeom<D>;
   constexpr int kPer = kKvThreads / Gm::kLanes;
-  __shared__ long long where[kKvGatherRows];
-  __shared__ int first_seq;
+  __shared__ long long where[Rows];
+  __shared__ int seq_of[Rows];
   grid_launch_dependents();
   grid_dependency_wait();
-  const long long r0 = static_cast<long long>(blockIdx.x) * kKvGatherRows;
-  // the sequence of row r0: the number of sequences that end at or before it
-  int ended = 0;
-  for (int i = threadIdx.x; i < p.seqs; i += kKvThreads) ended += __ldg(p.cu + i + 1) <= r0;
-  if (threadIdx.x == 0) first_seq = 0;
+  const long long r0 = static_cast<long long>(blockIdx.x) * Rows;
+  if (threadIdx.x < Rows) seq_of[threadIdx.x] = -1;
   __syncthreads();
-  ended = __reduce_add_sync(0xffffffffu, ended);
-  if ((threadIdx.x & 31) == 0 && ended) atomicAdd(&first_seq, ended);
+  // sequences mark the row that they begin at, or the first row if they began before it; a row's
+  // sequence is the last mark up to it
+  for (int s = threadIdx.x; s < p.seqs; s += kKvThreads) {
+    const long long a = max(r0, static_cast<long long>(__ldg(p.cu + s)));
+    if (a < r0 + Rows && a < __ldg(p.cu + s + 1)) atomicMax(&seq_of[a - r0], s);
+  }
   __syncthreads();
-  if (threadIdx.x < kKvGatherRows) {
+  if (threadIdx.x < (Rows + 31) / 32 * 32) {
     const long long r = r0 + threadIdx.x;
+    int s = threadIdx.x < Rows ? seq_of[threadIdx.x] : -1;
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, s, x);
+      if ((threadIdx.x & 31) >= x) s = max(s, y);
+    }
+    for (int w = threadIdx.x & ~31; w > 0; w -= 32) s = max(s, __reduce_max_sync(0xffffffffu, seq_of[w - 32 + (threadIdx.x & 31)]));
+    if (s >= 0 && r >= __ldg(p.cu + s + 1)) s = -1;
     long long at = -1;
-    if (r < p.rows) {
-      int s = first_seq;
-      while (s < p.seqs && __ldg(p.cu + s + 1) <= r) ++s;
-      if (s < p.seqs) {
-        const int lo = __ldg(p.cu + s), t0 = p.first != nullptr ? __ldg(p.first + s) : 0;
-        const long long t = t0 + (r - lo);
-        if (r < lo || t0 < 0 || t / p.page_tokens >= p.width) {
-          kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
+    if (threadIdx.x < Rows && r < p.rows && s >= 0) {
+      const long long t0 = p.first != nullptr ? __ldg(p.first + s) : 0, t = t0 + (r - __ldg(p.cu + s));
+      const int index = static_cast<int>(div64(t, p.page_tokens));
+      if (t0 < 0 || index >= p.width) {
+        kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
+      } else {
+        const int page = __ldg(p.table + static_cast<long long>(s) * p.width + index);
+        if (page < 0 || page >= p.pages) {
+          kv_error(p.err, FMOE_DEVERR_BAD_PAGE);
         } else {
-          const int page = __ldg(p.table + static_cast<long long>(s) * p.width + t / p.page_tokens);
-          if (page < 0 || page >= p.pages) {
-            kv_error(p.err, FMOE_DEVERR_BAD_PAGE);
-          } else {
-            const int place = static_cast<int>(t % p.page_tokens);
-            at = page * p.page_bytes + static_cast<long long>(place / kKvTile) * Gm::kTileBytes + place % kKvTile;
-          }
+          const int place = static_cast<int>(t - static_cast<long long>(index) * p.page_tokens);
+          at = page * p.page_bytes + static_cast<long long>(place / kKvTile) * Gm::kTileBytes + place % kKvTile;
         }
       }
     }
-    where[threadIdx.x] = at;
+    if (threadIdx.x < Rows) where[threadIdx.x] = at;
   }
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && __ldg(p.cu + p.seqs) > p.rows)
     kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
@@ -239,24 +299,35 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const __grid_cons
   const int lane = threadIdx.x % Gm::kLanes, grp = threadIdx.x / Gm::kLanes;
   const long long head_bytes = static_cast<long long>(p.page_tokens / kKvTile) * Gm::kTileBytes;
   for (int h = blockIdx.y; h < p.kv_heads; h += gridDim.y) {
+    constexpr int kTasks = 2 * Rows / kPer, kAhead = 8;
 #pragma unroll
-    for (int i = grp; i < 2 * kKvGatherRows; i += kPer) {
-      const int rr = i >> 1;
-      const bool val = i & 1;
-      const long long at = where[rr];
-      if (at < 0) continue;
-      // page and tile offsets are multiples of 16, the row in the tile rides in the low bits
-      const int row = static_cast<int>(at & 15);
-      const uint8_t* tile = p.cache + (at - row) + h * head_bytes;
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffV : 0) + row * Gm::kRow) + (lane & 7) * Gm::kGroups + lane / 8);
-      const uint32_t sb = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffVs : Gm::kOffKs)) + row * Gm::kGroups + lane / 8);
-      const float s = sb_scale(sb), b = sb_bias(sb);
-      uint32_t o[4];
+    for (int i0 = 0; i0 < kTasks; i0 += kAhead) {
+      uint32_t w[kAhead], sb[kAhead];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        o[c] = pack_bf16(fmaf(s, static_cast<float>((w >> (8 * c)) & 15u), b), fmaf(s, static_cast<float>((w >> (8 * c + 4)) & 15u), b));
-      uint16_t* dst = (val ? p.v_out : p.k_out) + ((r0 + rr) * p.kv_heads + h) * D + lane * 8;
-      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int u = 0; u < kAhead && i0 + u < kTasks; ++u) {
+        const int i = (i0 + u) * kPer + grp, rr = i >> 1;
+        const bool val = i & 1;
+        const long long at = where[rr];
+        w[u] = sb[u] = 0;
+        if (at < 0) continue;
+        // page and tile offsets are multiples of 16, the row in the tile rides in the low bits
+        const int row = static_cast<int>(at & 15);
+        const uint8_t* tile = p.cache + (at - row) + h * head_bytes;
+        w[u] = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffV : 0) + row * Gm::kRow) + (lane & 7) * Gm::kGroups + lane / 8);
+        sb[u] = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffVs : Gm::kOffKs)) + row * Gm::kGroups + lane / 8);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead && i0 + u < kTasks; ++u) {
+        const int i = (i0 + u) * kPer + grp, rr = i >> 1;
+        if (where[rr] < 0) continue;
+        const float s = sb_scale(sb[u]), b = sb_bias(sb[u]);
+        uint32_t o[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          o[c] = pack_bf16(fmaf(s, static_cast<float>((w[u] >> (8 * c)) & 15u), b), fmaf(s, static_cast<float>((w[u] >> (8 * c + 4)) & 15u), b));
+        uint16_t* dst = (i & 1 ? p.v_out : p.k_out) + ((r0 + rr) * p.kv_heads + h) * D + lane * 8;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
 }
