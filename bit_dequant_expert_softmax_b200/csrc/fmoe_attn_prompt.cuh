@@ -65,7 +65,7 @@ struct ApGeom {
 struct ApBars {
   uint64_t q_full[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: the first and the second half of the keys
   uint64_t drain;
   int abort_flag;
   uint32_t tmem;
@@ -134,19 +134,46 @@ __device__ __forceinline__ uint64_t ap_desc(uint32_t saddr, uint32_t lbo) {
 __device__ __forceinline__ uint32_t ap_idesc(int n, bool b_trans) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_trans ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
-// D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[smem or tmem] B[smem], and the commit of all products so far to `bar`, by the lane
+// that has `leads`.  The whole warp comes here, converged, so that addresses and descriptors stay
+// in uniform registers, where the instructions take them from.
+__device__ __forceinline__ void ap_mma_ss(uint32_t leads, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leads)
       : "memory");
 }
+__device__ __forceinline__ void ap_mma_ts(uint32_t leads, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leads)
+      : "memory");
+}
+__device__ __forceinline__ void ap_commit(uint32_t leads, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leads)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is;
+}
+
+// 32 or 128 columns of the lane's row, landed: load and wait are one statement, so that nothing
+// can use a register before it holds its value.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+      "%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
       : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
         "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
         "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
@@ -154,14 +181,52 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
       : "r"(taddr)
       : "memory");
 }
-
-// Behind the wait for a load: no use of its registers is moved before it.
-__device__ __forceinline__ void tmem_landed32(float* v) {
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
-  asm volatile("" : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
-                    "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]));
-  asm volatile("" : "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]),
-                    "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]), "+r"(u[30]), "+r"(u[31]));
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+      "%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,"
+      "%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,"
+      "%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,"
+      "%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,"
+      "%121,%122,%123,%124,%125,%126,%127}, [%128];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31]), "=r"(u[32]),
+        "=r"(u[33]), "=r"(u[34]), "=r"(u[35]), "=r"(u[36]), "=r"(u[37]), "=r"(u[38]), "=r"(u[39]), "=r"(u[40]),
+        "=r"(u[41]), "=r"(u[42]), "=r"(u[43]), "=r"(u[44]), "=r"(u[45]), "=r"(u[46]), "=r"(u[47]), "=r"(u[48]),
+        "=r"(u[49]), "=r"(u[50]), "=r"(u[51]), "=r"(u[52]), "=r"(u[53]), "=r"(u[54]), "=r"(u[55]), "=r"(u[56]),
+        "=r"(u[57]), "=r"(u[58]), "=r"(u[59]), "=r"(u[60]), "=r"(u[61]), "=r"(u[62]), "=r"(u[63]), "=r"(u[64]),
+        "=r"(u[65]), "=r"(u[66]), "=r"(u[67]), "=r"(u[68]), "=r"(u[69]), "=r"(u[70]), "=r"(u[71]), "=r"(u[72]),
+        "=r"(u[73]), "=r"(u[74]), "=r"(u[75]), "=r"(u[76]), "=r"(u[77]), "=r"(u[78]), "=r"(u[79]), "=r"(u[80]),
+        "=r"(u[81]), "=r"(u[82]), "=r"(u[83]), "=r"(u[84]), "=r"(u[85]), "=r"(u[86]), "=r"(u[87]), "=r"(u[88]),
+        "=r"(u[89]), "=r"(u[90]), "=r"(u[91]), "=r"(u[92]), "=r"(u[93]), "=r"(u[94]), "=r"(u[95]), "=r"(u[96]),
+        "=r"(u[97]), "=r"(u[98]), "=r"(u[99]), "=r"(u[100]), "=r"(u[101]), "=r"(u[102]), "=r"(u[103]), "=r"(u[104]),
+        "=r"(u[105]), "=r"(u[106]), "=r"(u[107]), "=r"(u[108]), "=r"(u[109]), "=r"(u[110]), "=r"(u[111]),
+        "=r"(u[112]), "=r"(u[113]), "=r"(u[114]), "=r"(u[115]), "=r"(u[116]), "=r"(u[117]), "=r"(u[118]),
+        "=r"(u[119]), "=r"(u[120]), "=r"(u[121]), "=r"(u[122]), "=r"(u[123]), "=r"(u[124]), "=r"(u[125]),
+        "=r"(u[126]), "=r"(u[127])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// two floats at once: a b + c, a + b
+__device__ __forceinline__ unsigned long long ffma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long fadd2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 template <int D>
@@ -227,50 +292,60 @@ struct ApBlock {
     return true;
   }
 
-  // ---- products: one lane.  Products of one thread run in the order of their issue, so
-  // S(j + 1) may be issued behind the product that reads P(j) from the same columns.
-  __device__ __forceinline__ bool score(int x, int j, uint32_t tmem) {
-    const int s = j % Gm::kStages;
-    if (!wait(&bar->k_full[s], (j / Gm::kStages) & 1)) return false;
-    tc_fence_after();
+  // ---- products: the whole warp, one lane issuing.  Products of one thread run in the order of
+  // their issue, so S(j + 1) may be issued behind the product that reads P(j) from the same columns.
+  __device__ __forceinline__ bool all(bool ok) const { return __all_sync(0xffffffffu, ok); }
+  __device__ __forceinline__ bool keys(int j) const { return all(wait(&bar->k_full[j % Gm::kStages], (j / Gm::kStages) & 1)); }
+  __device__ __forceinline__ void score(uint32_t leads, int x, int j, uint32_t tmem, uint32_t smem) {
     const uint32_t idesc = ap_idesc(kApKeys, false);
-    const uint64_t a = ap_desc(smem_u32(q_at(x)), 16), b = ap_desc(smem_u32(k_at(s)), 16);
+    const uint64_t a = ap_desc(smem + Gm::kQ + x * Gm::kHalves * Gm::kBlock, 16);
+    const uint64_t b = ap_desc(smem + Gm::kK + j % Gm::kStages * Gm::kHalves * Gm::kBlock, 16);
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       const uint64_t at = (static_cast<uint64_t>(c / 4) * Gm::kBlock + (c % 4) * 32) >> 4;
-      umma_ss(tmem + Gm::kTmemS + 128 * x, a + at, b + at, idesc, c > 0);
+      ap_mma_ss(leads, tmem + Gm::kTmemS + 128 * x, a + at, b + at, idesc, c > 0);
     }
-    umma_commit(&bar->s_full[x]);
-    return true;
+    ap_commit(leads, &bar->s_full[x]);
   }
-  __device__ __forceinline__ bool value(int x, int j, uint32_t tmem) {
-    const int s = j % Gm::kStages;
-    if (!wait(&bar->p_full[x], j & 1) || !wait(&bar->v_full[s], (j / Gm::kStages) & 1)) return false;
-    tc_fence_after();
+  // half h of the keys
+  __device__ __forceinline__ void value(uint32_t leads, int x, int j, int h, uint32_t tmem, uint32_t smem) {
     const uint32_t idesc = ap_idesc(D, true);
-    const uint64_t b = ap_desc(smem_u32(v_at(s)), Gm::kBlock);
+    const uint64_t b = ap_desc(smem + Gm::kV + j % Gm::kStages * Gm::kHalves * Gm::kBlock, Gm::kBlock);
 #pragma unroll
-    for (int c = 0; c < kApKeys / 16; ++c)
-      umma_ts(tmem + Gm::kTmemO + D * x, tmem + Gm::kTmemS + 128 * x + 8 * c, b + ((c * 2048) >> 4), idesc, j > 0 || c > 0);
-    umma_commit(&bar->o_full[x]);
-    return true;
+    for (int c = 4 * h; c < 4 * h + 4; ++c)
+      ap_mma_ts(leads, tmem + Gm::kTmemO + D * x, tmem + Gm::kTmemS + 128 * x + 8 * c, b + ((c * 2048) >> 4), idesc, j > 0 || c > 0);
+    if (h == 1) ap_commit(leads, &bar->o_full[x]);
   }
-  __device__ void multiply(uint32_t tmem) {
-    const int n = max(steps[0], steps[1]);
-    bool ok = true;
-    for (int x = 0; x < 2 && ok; ++x)
-      if (steps[x] > 0) ok = wait(&bar->q_full[x], 0) && score(x, 0, tmem);
-    if (ok) umma_commit(&bar->k_empty[0]);
+  __device__ void multiply(uint32_t tmem_any) {
+    const uint32_t leads = elect_lane();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0), smem = __shfl_sync(0xffffffffu, smem_u32(base), 0);
+    const int n0 = __shfl_sync(0xffffffffu, steps[0], 0), n1 = __shfl_sync(0xffffffffu, steps[1], 0), n = max(n0, n1);
+    bool ok = keys(0) && all((n0 == 0 || wait(&bar->q_full[0], 0)) && (n1 == 0 || wait(&bar->q_full[1], 0)));
+    if (ok) {
+      tc_fence_after();
+      if (n0 > 0) score(leads, 0, 0, tmem, smem);
+      if (n1 > 0) score(leads, 1, 0, tmem, smem);
+      ap_commit(leads, &bar->k_empty[0]);
+    }
     for (int j = 0; j < n && ok; ++j) {
+      const bool more = j + 1 < n;
+      ok = all(wait(&bar->v_full[j % Gm::kStages], (j / Gm::kStages) & 1)) && (!more || keys(j + 1));
       for (int x = 0; x < 2 && ok; ++x) {
-        if (j < steps[x]) ok = value(x, j, tmem);
-        if (ok && j + 1 < steps[x]) ok = score(x, j + 1, tmem);
+        const int nx = x ? n1 : n0;
+        if (j >= nx) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || !(ok = all(wait(&bar->p_full[x][h], j & 1)))) break;
+          tc_fence_after();
+          value(leads, x, j, h, tmem, smem);
+        }
+        if (ok && j + 1 < nx) score(leads, x, j + 1, tmem, smem);
       }
       if (!ok) break;
-      umma_commit(&bar->v_empty[j % Gm::kStages]);
-      if (j + 1 < n) umma_commit(&bar->k_empty[(j + 1) % Gm::kStages]);
+      ap_commit(leads, &bar->v_empty[j % Gm::kStages]);
+      if (more) ap_commit(leads, &bar->k_empty[(j + 1) % Gm::kStages]);
     }
-    umma_commit(&bar->drain);  // nothing reads or writes tensor memory after this
+    ap_commit(leads, &bar->drain);  // nothing reads or writes tensor memory after this
     wait(&bar->drain, 0, true);
   }
 
@@ -289,11 +364,7 @@ struct ApBlock {
       if (!__all_sync(0xffffffffu, wait(&bar->s_full[x], j & 1))) return;
       tc_fence_after();
       float s[kApKeys];
-#pragma unroll
-      for (int i = 0; i < kApKeys; i += 32) tmem_ld32(ts + i, s + i);
-      tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < kApKeys; i += 32) tmem_landed32(s + i);
+      tmem_ld128(ts, s);
       if (p.scale_log2 < 0.f) {
 #pragma unroll
         for (int i = 0; i < kApKeys; ++i) s[i] = -s[i];
@@ -305,8 +376,13 @@ struct ApBlock {
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int i = 4; i < kApKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      for (int i = 4; i < kApKeys - 4; i += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kApKeys - 4 + e]);
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       const bool far = ref == -INFINITY ? top > -INFINITY : top - ref > slack;
       if (__any_sync(0xffffffffu, far)) {
         const float now = far ? top : ref;
@@ -320,33 +396,14 @@ struct ApBlock {
           for (int i = 0; i < D; i += 32) {
             float o[32];
             tmem_ld32(to + i, o);
-            tmem_wait_ld();
-            tmem_landed32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
             uint32_t w[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
             tmem_st32(to + i, w);
           }
         }
         ref = now;
       }
-      const float off = ref == -INFINITY ? 0.f : -ref * c;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = ex2(fmaf(s[64 * h + 2 * i], c, off)), b = ex2(fmaf(s[64 * h + 2 * i + 1], c, off));
-          sum[2 * (i & 1)] += a;
-          sum[2 * (i & 1) + 1] += b;
-          w[i] = pack_bf16(a, b);
-        }
-        tmem_st32(ts + 32 * h, w);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if ((j + 1) * kApKeys > T.nk) {  // the sequence's last, partial step: V behind it as zeros
         if (!__all_sync(0xffffffffu, wait(&bar->v_full[j % Gm::kStages], (j / Gm::kStages) & 1))) return;
         const int first = T.nk - j * kApKeys;
@@ -356,13 +413,29 @@ struct ApBlock {
         }
         fence_proxy_async_smem();
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->p_full[x]);
+      const float off = ref == -INFINITY ? 0.f : -ref * c;
+      const unsigned long long c2 = pack2(c, c), off2 = pack2(off, off);
+      unsigned long long sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const unsigned long long x2 = ffma2(pack2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), c2, off2);
+          const float a = ex2(__uint_as_float(static_cast<uint32_t>(x2))), b = ex2(__uint_as_float(static_cast<uint32_t>(x2 >> 32)));
+          sum[i & 1] = fadd2(sum[i & 1], pack2(a, b));
+          w[i] = pack_bf16(a, b);
+        }
+        tmem_st32(ts + 32 * h, w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->p_full[x][h]);
+      }
+      l += pair_sum(fadd2(sum[0], sum[1]));
     }
-    // the output rows (zeros where a row has seen nothing)
-    uint16_t* dst = p.out + ((static_cast<long long>(T.q0) + tok) * p.q_heads + head) * D;
+    // the output rows (zeros where a row has seen nothing), through the tile's Q rows, which the
+    // last score product has read, so that a row's bytes leave together
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (steps[x] > 0) {
       if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (steps[x] - 1) & 1))) return;
@@ -373,19 +446,25 @@ struct ApBlock {
       float o[32];
       if (steps[x] > 0) {
         tmem_ld32(to + i, o);
-        tmem_wait_ld();
-        tmem_landed32(o);
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0.f;
       }
-      if (live) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(dst + i + e) =
-              make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                         pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-      }
+      for (int e = 0; e < 32; e += 8)
+        *reinterpret_cast<uint4*>(q_at(x) + (i / 64) * Gm::kBlock + row * 128 + ((((i + e) % 64 / 8) ^ (row & 7)) << 4)) =
+            make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                       pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+    }
+    __syncwarp();
+    const long long mine = live ? ((static_cast<long long>(T.q0) + tok) * p.q_heads + head) * D : -1;
+    constexpr int kLanes = D / 8;  // of a row
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) {
+      const int from = i * (32 / kLanes) + lane / kLanes, r = (row & ~31) + from, e = lane % kLanes;
+      const long long at = __shfl_sync(0xffffffffu, mine, from);
+      const uint4 v = *reinterpret_cast<const uint4*>(q_at(x) + (e / 8) * Gm::kBlock + r * 128 + (((e % 8) ^ (r & 7)) << 4));
+      if (at >= 0) *reinterpret_cast<uint4*>(p.out + at + 8 * e) = v;
     }
     tc_fence_before();
   }
@@ -415,7 +494,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_prompt_kernel(const __grid
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->q_full[i], 1);
       mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->p_full[i], 4);
+      mbar_init(&bar->p_full[i][0], 4);
+      mbar_init(&bar->p_full[i][1], 4);
       mbar_init(&bar->o_full[i], 1);
     }
     for (int i = 0; i < Gm::kStages; ++i) {
@@ -442,9 +522,9 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_prompt_kernel(const __grid
     B.soften(warp >> 2, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (max(B.steps[0], B.steps[1]) > 0 && lane == 0) {
+    if (max(B.steps[0], B.steps[1]) > 0) {
       if (warp == kApMmaWarp) B.multiply(tmem);
-      if (warp == kApLoadWarp) B.load();
+      if (warp == kApLoadWarp && lane == 0) B.load();
     }
   }
   tc_fence_before();

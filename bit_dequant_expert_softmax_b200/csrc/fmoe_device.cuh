@@ -194,6 +194,10 @@ __device__ __forceinline__ void fma2(unsigned long long& acc, unsigned long long
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(c), "l"(x));
 }
 
+__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
+  return (static_cast<unsigned long long>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+}
+
 __device__ __forceinline__ float pair_sum(unsigned long long a) {
   return __uint_as_float(static_cast<uint32_t>(a)) + __uint_as_float(static_cast<uint32_t>(a >> 32));
 }

@@ -142,10 +142,6 @@ __host__ __device__ constexpr uint32_t umma_smem_bytes(int slots) {
 }
 
 // ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
-  return (static_cast<unsigned long long>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
-}
-
 // Shared-memory matrix descriptor, K-major, no swizzle: core matrices of 8 rows x 16 B
 // (rows 16 B apart), `lbo` bytes between the two 8-element K halves, `sbo` bytes
 // between 8-row groups; descriptor version 1.
