@@ -14,6 +14,9 @@ using namespace fmoe;
 namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
+#ifndef PAIRS
+#define PAIRS 0
+#endif
 constexpr int kMaxGridY = 65535;
 constexpr int kFewTokens = 480;  // fmoe_kv_append: 300 tokens of 32 + 2 x 4 heads take 6.3 us by blocks, 8.1 by warps; 600: 9.8, 8.5
 constexpr int kGatherWide = 400;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 5.5 us 64 rows a block, 4.8 us 16; 4000: 6.9, 7.6
@@ -147,12 +150,16 @@ bool row_map(CUtensorMap* m, const uint16_t* base, int D, int heads, int64_t row
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-fmoe_status prompt(const ApParams& p, void* stream) {
+template <int D, int X>
+fmoe_status prompt(ApParams& p, int64_t q_rows, int device, void* stream) {
   static std::atomic<uint64_t> done{0};
-  int device = 0;
-  if (device_sms(&device) == 0 || !opt_in(attn_prompt_kernel<D>, ApGeom<D>::kSmem, device, done)) return FMOE_ERR_CUDA;
-  return launch(attn_prompt_kernel<D>, dim3((unsigned)(p.units * p.kv_heads)), kApThreads, ApGeom<D>::kSmem, stream, p);
+  using Gm = ApGeom<D, X>;
+  // units of X tiles of queries: at most this many over all sequences
+  const int64_t units = q_rows / (X * p.tile_tokens) + p.seqs;
+  if (units * p.kv_heads > INT32_MAX) return FMOE_ERR_UNSUPPORTED;
+  p.units = (int)units;
+  if (!opt_in(attn_prompt_kernel<D, X>, Gm::kSmem, device, done)) return FMOE_ERR_CUDA;
+  return launch(attn_prompt_kernel<D, X>, dim3((unsigned)(units * p.kv_heads)), Gm::kThreads, Gm::kSmem, stream, p);
 }
 
 }  // namespace
@@ -291,10 +298,6 @@ fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64
   const int G = c->q_heads / c->kv_heads;
   ApParams p{};
   p.tile_tokens = kApRows / G;
-  // units of 2 tile_tokens queries: at most this many over all sequences
-  const int64_t units = q_rows / (2 * p.tile_tokens) + seqs;
-  if (units * c->kv_heads > INT32_MAX) return FMOE_ERR_UNSUPPORTED;
-  p.units = (int)units;
   if (!row_map(&p.tm_q, q, D, c->q_heads, q_rows, q_stride, G, p.tile_tokens) ||
       !row_map(&p.tm_k, k, D, c->kv_heads, k_rows, k_stride, 1, kApKeys) ||
       !row_map(&p.tm_v, v, D, c->kv_heads, k_rows, v_stride, 1, kApKeys))
@@ -303,7 +306,11 @@ fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64
   p.cu_q = cu_q, p.cu_k = cu_k, p.out = out, p.err = device_error;
   p.scale_log2 = (float)(scale * kLog2e);
   p.seqs = seqs, p.q_heads = c->q_heads, p.kv_heads = c->kv_heads, p.group = G;
-  return D == 128 ? prompt<128>(p, stream) : prompt<64>(p, stream);
+  int device = 0;
+  if (device_sms(&device) == 0) return FMOE_ERR_CUDA;
+  const bool pairs = PAIRS;
+  if (D == 128) return pairs ? prompt<128, 2>(p, q_rows, device, stream) : prompt<128, 1>(p, q_rows, device, stream);
+  return pairs ? prompt<64, 2>(p, q_rows, device, stream) : prompt<64, 1>(p, q_rows, device, stream);
 }
 
 }  // extern "C"

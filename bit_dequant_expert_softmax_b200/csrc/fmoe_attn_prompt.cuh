@@ -34,8 +34,6 @@ namespace fmoe {
 
 constexpr int kApRows = 128;                 // rows of a tile
 constexpr int kApKeys = 128;                 // keys of a step
-constexpr int kApThreads = 384;
-constexpr int kApMmaWarp = 8, kApLoadWarp = 9;
 constexpr unsigned long long kApWaitNs = 2000000000ull;
 constexpr float kApSlack = 8.f;              // log2 units a row's maximum may pass its reference by
 
@@ -49,17 +47,25 @@ struct alignas(64) ApParams {
   int seqs, q_heads, kv_heads, group, tile_tokens, units;
 };
 
-template <int D>
+// X row tiles per block
+template <int D, int X>
 struct ApGeom {
   static constexpr int kHalves = D / 64;               // 128-byte wide column blocks
   static constexpr int kBlock = 128 * 128;             // 128 rows of 128 bytes
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kQ = 0;                         // [2 tiles][halves]
-  static constexpr int kK = kQ + 2 * kHalves * kBlock; // [stages][halves]
+  static constexpr int kStages = (D == 128 ? 1 : 2) * X;
+  static constexpr int kMmaWarp = 4 * X, kLoadWarp = 4 * X + 1, kThreads = X == 2 ? 384 : 192;
+  static constexpr int kBlocks = 3 - X;                // on an SM
+  static constexpr int kQ = 0;                         // [tiles][halves]
+  static constexpr int kK = kQ + X * kHalves * kBlock; // [stages][halves]
   static constexpr int kV = kK + kStages * kHalves * kBlock;
   static constexpr int kBars = kV + kStages * kHalves * kBlock;
   static constexpr int kSmem = kBars + 512 + 1024;     // + alignment
-  static constexpr uint32_t kTmemS = 0, kTmemO = 256;  // columns: S of tile x at 128 x, O at 256 + D x
+  // Registers: two blocks of 192 threads leave a thread 168, so a softmax thread has 64 scores at a
+  // time and loads the first half of a step twice (for the maximum and for the weights); one block
+  // lets the softmax warps take more, and they hold a step's 128.
+  static constexpr bool kTwice = X == 1;
+  static constexpr uint32_t kP = kTwice ? 64 : 32;     // columns from P of the first half to the second's
+  static constexpr uint32_t kTmemS = 0, kTmemO = 128 * X, kTmem = 256 * X;  // columns: S of tile x at 128 x, O behind them at D x
 };
 
 struct ApBars {
@@ -130,9 +136,9 @@ __device__ __forceinline__ uint64_t ap_desc(uint32_t saddr, uint32_t lbo) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
          (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// bf16 x bf16 -> f32, M = 128, N = n, B transposed or not
-__device__ __forceinline__ uint32_t ap_idesc(int n, bool b_trans) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_trans ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+// bf16 x bf16 -> f32, M = 128, N = n, A negated or not, B transposed or not
+__device__ __forceinline__ uint32_t ap_idesc(int n, bool a_neg, bool b_trans) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_neg ? 1u << 13 : 0u) | (b_trans ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 // D[tmem] (+)= A[smem or tmem] B[smem], and the commit of all products so far to `bar`, by the lane
 // that has `leads`.  The whole warp comes here, converged, so that addresses and descriptors stay
@@ -166,7 +172,7 @@ __device__ __forceinline__ uint32_t elect_lane() {
   return is;
 }
 
-// 32 or 128 columns of the lane's row, landed: load and wait are one statement, so that nothing
+// 32, 64 or 128 columns of the lane's row, landed: load and wait are one statement, so that nothing
 // can use a register before it holds its value.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
@@ -178,6 +184,24 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
         "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
         "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
         "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+      "%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,"
+      "%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31]), "=r"(u[32]),
+        "=r"(u[33]), "=r"(u[34]), "=r"(u[35]), "=r"(u[36]), "=r"(u[37]), "=r"(u[38]), "=r"(u[39]), "=r"(u[40]),
+        "=r"(u[41]), "=r"(u[42]), "=r"(u[43]), "=r"(u[44]), "=r"(u[45]), "=r"(u[46]), "=r"(u[47]), "=r"(u[48]),
+        "=r"(u[49]), "=r"(u[50]), "=r"(u[51]), "=r"(u[52]), "=r"(u[53]), "=r"(u[54]), "=r"(u[55]), "=r"(u[56]),
+        "=r"(u[57]), "=r"(u[58]), "=r"(u[59]), "=r"(u[60]), "=r"(u[61]), "=r"(u[62]), "=r"(u[63])
       : "r"(taddr)
       : "memory");
 }
@@ -229,15 +253,15 @@ __device__ __forceinline__ unsigned long long fadd2(unsigned long long a, unsign
   return d;
 }
 
-template <int D>
+template <int D, int X>
 struct ApBlock {
-  using Gm = ApGeom<D>;
+  using Gm = ApGeom<D, X>;
   const ApParams& p;
   uint8_t* base;
   ApBars* bar;
   ApTile T;
   int kvh;
-  int steps[2];  // key steps of the two row tiles
+  int steps[X];  // key steps of the row tiles
 
   __device__ __forceinline__ uint8_t* q_at(int x) const { return base + Gm::kQ + x * Gm::kHalves * Gm::kBlock; }
   __device__ __forceinline__ uint8_t* k_at(int s) const { return base + Gm::kK + s * Gm::kHalves * Gm::kBlock; }
@@ -262,22 +286,24 @@ struct ApBlock {
   // ---- loads: one lane
   __device__ void load() {
     const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * 128u;
-    for (int x = 0; x < 2; ++x) {
+    int n = 0;
+    for (int x = 0; x < X; ++x) n = max(n, steps[x]);
+    bool first = true;
+    for (int x = 0; x < X; ++x) {
       if (steps[x] == 0) continue;
       mbar_arrive_expect_tx(&bar->q_full[x], q_bytes * Gm::kHalves);
       for (int h = 0; h < Gm::kHalves; ++h)
         tma_load_3d(q_at(x) + h * Gm::kBlock, &p.tm_q, &bar->q_full[x], 64 * h, kvh * p.group, T.q0 + T.first + x * p.tile_tokens);
-      if (x == 0) load_kv(0, true);
+      if (first) load_kv(0, true);
+      first = false;
     }
-    const int n = max(steps[0], steps[1]);
-    if (steps[0] == 0) load_kv(0, true);
     int k = 1, v = 0;  // loads issued
     while (v < n && load_kv(v, false)) {
       if (++v == n || !load_kv(k, true)) break;
       ++k;
     }
     // copies still in flight land before the block ends
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < X; ++x)
       if (steps[x] > 0) wait(&bar->q_full[x], 0, true);
     for (int i = max(0, k - Gm::kStages); i < k; ++i) wait(&bar->k_full[i % Gm::kStages], (i / Gm::kStages) & 1, true);
     for (int i = max(0, v - Gm::kStages); i < v; ++i) wait(&bar->v_full[i % Gm::kStages], (i / Gm::kStages) & 1, true);
@@ -297,7 +323,7 @@ struct ApBlock {
   __device__ __forceinline__ bool all(bool ok) const { return __all_sync(0xffffffffu, ok); }
   __device__ __forceinline__ bool keys(int j) const { return all(wait(&bar->k_full[j % Gm::kStages], (j / Gm::kStages) & 1)); }
   __device__ __forceinline__ void score(uint32_t leads, int x, int j, uint32_t tmem, uint32_t smem) {
-    const uint32_t idesc = ap_idesc(kApKeys, false);
+    const uint32_t idesc = ap_idesc(kApKeys, p.scale_log2 < 0.f, false);  // the softmax goes by |scale|
     const uint64_t a = ap_desc(smem + Gm::kQ + x * Gm::kHalves * Gm::kBlock, 16);
     const uint64_t b = ap_desc(smem + Gm::kK + j % Gm::kStages * Gm::kHalves * Gm::kBlock, 16);
 #pragma unroll
@@ -307,39 +333,48 @@ struct ApBlock {
     }
     ap_commit(leads, &bar->s_full[x]);
   }
-  // half h of the keys
-  __device__ __forceinline__ void value(uint32_t leads, int x, int j, int h, uint32_t tmem, uint32_t smem) {
-    const uint32_t idesc = ap_idesc(D, true);
+  // half h of the keys, the first or the second of the two
+  __device__ __forceinline__ void value(uint32_t leads, int x, int j, int h, bool first, uint32_t tmem, uint32_t smem) {
+    const uint32_t idesc = ap_idesc(D, false, true);
     const uint64_t b = ap_desc(smem + Gm::kV + j % Gm::kStages * Gm::kHalves * Gm::kBlock, Gm::kBlock);
 #pragma unroll
     for (int c = 4 * h; c < 4 * h + 4; ++c)
-      ap_mma_ts(leads, tmem + Gm::kTmemO + D * x, tmem + Gm::kTmemS + 128 * x + 8 * c, b + ((c * 2048) >> 4), idesc, j > 0 || c > 0);
-    if (h == 1) ap_commit(leads, &bar->o_full[x]);
+      ap_mma_ts(leads, tmem + Gm::kTmemO + D * x, tmem + Gm::kTmemS + 128 * x + Gm::kP * h + 8 * (c % 4), b + ((c * 2048) >> 4), idesc,
+                j > 0 || first == 0 || c % 4 > 0);
+    if (!first) ap_commit(leads, &bar->o_full[x]);
   }
   __device__ void multiply(uint32_t tmem_any) {
     const uint32_t leads = elect_lane();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0), smem = __shfl_sync(0xffffffffu, smem_u32(base), 0);
-    const int n0 = __shfl_sync(0xffffffffu, steps[0], 0), n1 = __shfl_sync(0xffffffffu, steps[1], 0), n = max(n0, n1);
-    bool ok = keys(0) && all((n0 == 0 || wait(&bar->q_full[0], 0)) && (n1 == 0 || wait(&bar->q_full[1], 0)));
-    if (ok) {
-      tc_fence_after();
-      if (n0 > 0) score(leads, 0, 0, tmem, smem);
-      if (n1 > 0) score(leads, 1, 0, tmem, smem);
-      ap_commit(leads, &bar->k_empty[0]);
+    int nx[X], n = 0;
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      nx[x] = __shfl_sync(0xffffffffu, steps[x], 0);
+      n = max(n, nx[x]);
     }
+    bool ok = keys(0);
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      if (!ok || nx[x] == 0) continue;
+      ok = all(wait(&bar->q_full[x], 0));
+      tc_fence_after();
+      if (ok) score(leads, x, 0, tmem, smem);
+    }
+    ap_commit(leads, &bar->k_empty[0]);
     for (int j = 0; j < n && ok; ++j) {
       const bool more = j + 1 < n;
       ok = all(wait(&bar->v_full[j % Gm::kStages], (j / Gm::kStages) & 1)) && (!more || keys(j + 1));
-      for (int x = 0; x < 2 && ok; ++x) {
-        const int nx = x ? n1 : n0;
-        if (j >= nx) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+      for (int x = 0; x < X; ++x) {
+        if (!ok || j >= nx[x]) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int h = Gm::kTwice ? 1 - i : i;
           if (!ok || !(ok = all(wait(&bar->p_full[x][h], j & 1)))) break;
           tc_fence_after();
-          value(leads, x, j, h, tmem, smem);
+          value(leads, x, j, h, i == 0, tmem, smem);
         }
-        if (ok && j + 1 < nx) score(leads, x, j + 1, tmem, smem);
+        if (ok && j + 1 < nx[x]) score(leads, x, j + 1, tmem, smem);
       }
       if (!ok) break;
       ap_commit(leads, &bar->v_empty[j % Gm::kStages]);
@@ -363,26 +398,30 @@ struct ApBlock {
     for (int j = 0; j < steps[x]; ++j) {
       if (!__all_sync(0xffffffffu, wait(&bar->s_full[x], j & 1))) return;
       tc_fence_after();
-      float s[kApKeys];
-      tmem_ld128(ts, s);
-      if (p.scale_log2 < 0.f) {
+      constexpr int kHeld = Gm::kTwice ? 64 : kApKeys;
+      float s[kHeld];
+      auto take = [&](int from) {  // scores from .. of the step, those that the row does not see left out
+        if constexpr (Gm::kTwice)
+          tmem_ld64(ts + from, s);
+        else
+          tmem_ld128(ts, s);
+        const int lim = sees - j * kApKeys - from;
+        if (__any_sync(0xffffffffu, lim < kHeld)) {
 #pragma unroll
-        for (int i = 0; i < kApKeys; ++i) s[i] = -s[i];
-      }
-      const int lim = sees - j * kApKeys;
-      if (__any_sync(0xffffffffu, lim < kApKeys)) {
+          for (int i = 0; i < kHeld; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 0; i < kApKeys; ++i) s[i] = i < lim ? s[i] : -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+        for (int i = 4; i < kHeld - 4; i += 8) {
 #pragma unroll
-      for (int i = 4; i < kApKeys - 4; i += 8) {
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kApKeys - 4 + e]);
-      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kHeld - 4 + e]);
+        return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+      };
+      float top = take(0);
+      if constexpr (Gm::kTwice) top = fmaxf(top, take(64));
       const bool far = ref == -INFINITY ? top > -INFINITY : top - ref > slack;
       if (__any_sync(0xffffffffu, far)) {
         const float now = far ? top : ref;
@@ -392,7 +431,7 @@ struct ApBlock {
           // the products up to step j - 1 are in O
           if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (j - 1) & 1))) return;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1  // (rare)
           for (int i = 0; i < D; i += 32) {
             float o[32];
             tmem_ld32(to + i, o);
@@ -417,16 +456,18 @@ struct ApBlock {
       const unsigned long long c2 = pack2(c, c), off2 = pack2(off, off);
       unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int n = 0; n < 2; ++n) {
+        const int h = Gm::kTwice ? 1 - n : n, at = Gm::kTwice ? 0 : 64 * h;
+        if (Gm::kTwice && n == 1) take(0);
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const unsigned long long x2 = ffma2(pack2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), c2, off2);
+          const unsigned long long x2 = ffma2(pack2(s[at + 2 * i], s[at + 2 * i + 1]), c2, off2);
           const float a = ex2(__uint_as_float(static_cast<uint32_t>(x2))), b = ex2(__uint_as_float(static_cast<uint32_t>(x2 >> 32)));
           sum[i & 1] = fadd2(sum[i & 1], pack2(a, b));
           w[i] = pack_bf16(a, b);
         }
-        tmem_st32(ts + 32 * h, w);
+        tmem_st32(ts + Gm::kP * h, w);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -441,25 +482,24 @@ struct ApBlock {
       if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (steps[x] - 1) & 1))) return;
       tc_fence_after();
     }
-#pragma unroll
+    // rolled loops: this runs once, and unrolled it would wait for its instructions
+#pragma unroll 1
     for (int i = 0; i < D; i += 32) {
       float o[32];
-      if (steps[x] > 0) {
-        tmem_ld32(to + i, o);
-      } else {
+      tmem_ld32(to + i, o);
+      uint8_t* at = q_at(x) + (i / 64) * Gm::kBlock + row * 128;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      for (int e = 0; e < 32; e += 8) {
+        uint4 v = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                             pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+        if (steps[x] == 0) v = make_uint4(0u, 0u, 0u, 0u);  // O was never written
+        *reinterpret_cast<uint4*>(at + ((((i + e) % 64 / 8) ^ (row & 7)) << 4)) = v;
       }
-#pragma unroll
-      for (int e = 0; e < 32; e += 8)
-        *reinterpret_cast<uint4*>(q_at(x) + (i / 64) * Gm::kBlock + row * 128 + ((((i + e) % 64 / 8) ^ (row & 7)) << 4)) =
-            make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                       pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
     }
     __syncwarp();
     const long long mine = live ? ((static_cast<long long>(T.q0) + tok) * p.q_heads + head) * D : -1;
     constexpr int kLanes = D / 8;  // of a row
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < kLanes; ++i) {
       const int from = i * (32 / kLanes) + lane / kLanes, r = (row & ~31) + from, e = lane % kLanes;
       const long long at = __shfl_sync(0xffffffffu, mine, from);
@@ -472,26 +512,32 @@ struct ApBlock {
 
 // Blocks over (unit, key/value head), heads fastest and a sequence's last queries, which see
 // the most keys, first.
-template <int D>
-__global__ void __launch_bounds__(kApThreads, 1) attn_prompt_kernel(const __grid_constant__ ApParams p) {
-  using Gm = ApGeom<D>;
+template <int D, int X>
+__global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks) attn_prompt_kernel(const __grid_constant__ ApParams p) {
+  using Gm = ApGeom<D, X>;
   extern __shared__ uint8_t ap_smem[];
+  if (threadIdx.x < 3) {  // the maps on their way before the first load needs them
+    const CUtensorMap* map = threadIdx.x == 0 ? &p.tm_q : threadIdx.x == 1 ? &p.tm_k : &p.tm_v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+  }
   grid_launch_dependents();
   grid_dependency_wait();
   uint8_t* base = ap_smem + ((1024u - (smem_u32(ap_smem) & 1023u)) & 1023u);
-  ApBlock<D> B{p, base, reinterpret_cast<ApBars*>(base + Gm::kBars)};
-  if (!ap_find(p, p.units - 1 - static_cast<int>(blockIdx.x / p.kv_heads), 2 * p.tile_tokens, B.T)) return;
+  ApBlock<D, X> B{p, base, reinterpret_cast<ApBars*>(base + Gm::kBars)};
+  if (!ap_find(p, p.units - 1 - static_cast<int>(blockIdx.x / p.kv_heads), X * p.tile_tokens, B.T)) return;
   B.kvh = blockIdx.x % p.kv_heads;
+  bool some = false;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < X; ++x) {
     const int t0 = B.T.first + x * p.tile_tokens, last = min(B.T.nq, t0 + p.tile_tokens) - 1;
     const int keys = t0 < B.T.nq ? max(0, last + B.T.nk - B.T.nq + 1) : 0;
     B.steps[x] = (keys + kApKeys - 1) / kApKeys;
+    some |= keys > 0;
   }
   ApBars* bar = B.bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < X; ++i) {
       mbar_init(&bar->q_full[i], 1);
       mbar_init(&bar->s_full[i], 1);
       mbar_init(&bar->p_full[i][0], 4);
@@ -508,8 +554,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_prompt_kernel(const __grid
     bar->abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == kApMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar->tmem)), "r"(512)
+  if (warp == Gm::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar->tmem)), "r"(Gm::kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -517,20 +563,20 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_prompt_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar->tmem;
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  if (warp < 4 * X) {
+    if constexpr (X == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     B.soften(warp >> 2, tmem);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (max(B.steps[0], B.steps[1]) > 0) {
-      if (warp == kApMmaWarp) B.multiply(tmem);
-      if (warp == kApLoadWarp && lane == 0) B.load();
+    if constexpr (X == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (some) {
+      if (warp == Gm::kMmaWarp) B.multiply(tmem);
+      if (warp == Gm::kLoadWarp && lane == 0) B.load();
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kApMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  if (warp == Gm::kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Gm::kTmem) : "memory");
 }
 
 }  // namespace fmoe
