@@ -14,9 +14,6 @@ using namespace fmoe;
 namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
-#ifndef PAIRS
-#define PAIRS 0
-#endif
 constexpr int kMaxGridY = 65535;
 constexpr int kFewTokens = 480;  // fmoe_kv_append: 300 tokens of 32 + 2 x 4 heads take 6.3 us by blocks, 8.1 by warps; 600: 9.8, 8.5
 constexpr int kGatherWide = 400;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 5.5 us 64 rows a block, 4.8 us 16; 4000: 6.9, 7.6
@@ -307,8 +304,13 @@ fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64
   p.scale_log2 = (float)(scale * kLog2e);
   p.seqs = seqs, p.q_heads = c->q_heads, p.kv_heads = c->kv_heads, p.group = G;
   int device = 0;
-  if (device_sms(&device) == 0) return FMOE_ERR_CUDA;
-  const bool pairs = PAIRS;
+  const int sms = device_sms(&device);
+  if (sms == 0) return FMOE_ERR_CUDA;
+  // Two row tiles per block share the loads of K and V and want long sequences and blocks for
+  // every SM; one, with two blocks on an SM, hides a block's beginning and end under the other.
+  // Two against one, 32 over 8 heads of 128: 2048 tokens 40 and 45 us, 2 x 1024 28 and 32;
+  // 1024 (128 blocks of two) 20.4 and 19.2, 16 x 512 76.4 and 73.7, 333 11.6 and 11.0.
+  const bool pairs = k_rows / seqs >= 640 && q_rows / (2 * p.tile_tokens) * c->kv_heads >= sms;
   if (D == 128) return pairs ? prompt<128, 2>(p, q_rows, device, stream) : prompt<128, 1>(p, q_rows, device, stream);
   return pairs ? prompt<64, 2>(p, q_rows, device, stream) : prompt<64, 1>(p, q_rows, device, stream);
 }

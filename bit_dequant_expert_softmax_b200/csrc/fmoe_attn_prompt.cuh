@@ -261,7 +261,8 @@ struct ApBlock {
   ApBars* bar;
   ApTile T;
   int kvh;
-  int steps[X];  // key steps of the row tiles
+  int steps[X];    // key steps of the row tiles
+  bool short_[X];  // the last of them sees no key of its second half
 
   __device__ __forceinline__ uint8_t* q_at(int x) const { return base + Gm::kQ + x * Gm::kHalves * Gm::kBlock; }
   __device__ __forceinline__ uint8_t* k_at(int s) const { return base + Gm::kK + s * Gm::kHalves * Gm::kBlock; }
@@ -333,23 +334,25 @@ struct ApBlock {
     }
     ap_commit(leads, &bar->s_full[x]);
   }
-  // half h of the keys, the first or the second of the two
-  __device__ __forceinline__ void value(uint32_t leads, int x, int j, int h, bool first, uint32_t tmem, uint32_t smem) {
+  // half h of the keys, the first and / or the last that the step multiplies
+  __device__ __forceinline__ void value(uint32_t leads, int x, int j, int h, bool first, bool last, uint32_t tmem, uint32_t smem) {
     const uint32_t idesc = ap_idesc(D, false, true);
     const uint64_t b = ap_desc(smem + Gm::kV + j % Gm::kStages * Gm::kHalves * Gm::kBlock, Gm::kBlock);
 #pragma unroll
     for (int c = 4 * h; c < 4 * h + 4; ++c)
       ap_mma_ts(leads, tmem + Gm::kTmemO + D * x, tmem + Gm::kTmemS + 128 * x + Gm::kP * h + 8 * (c % 4), b + ((c * 2048) >> 4), idesc,
-                j > 0 || first == 0 || c % 4 > 0);
-    if (!first) ap_commit(leads, &bar->o_full[x]);
+                j > 0 || !first || c % 4 > 0);
+    if (last) ap_commit(leads, &bar->o_full[x]);
   }
   __device__ void multiply(uint32_t tmem_any) {
     const uint32_t leads = elect_lane();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0), smem = __shfl_sync(0xffffffffu, smem_u32(base), 0);
     int nx[X], n = 0;
+    bool cut[X];
 #pragma unroll
     for (int x = 0; x < X; ++x) {
       nx[x] = __shfl_sync(0xffffffffu, steps[x], 0);
+      cut[x] = __any_sync(0xffffffffu, short_[x]);
       n = max(n, nx[x]);
     }
     bool ok = keys(0);
@@ -370,9 +373,11 @@ struct ApBlock {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int h = Gm::kTwice ? 1 - i : i;
-          if (!ok || !(ok = all(wait(&bar->p_full[x][h], j & 1)))) break;
+          const bool one = cut[x] && j + 1 == nx[x];
+          if (!ok || (one && h == 1)) continue;
+          if (!(ok = all(wait(&bar->p_full[x][h], j & 1)))) continue;
           tc_fence_after();
-          value(leads, x, j, h, i == 0, tmem, smem);
+          value(leads, x, j, h, one || i == 0, one || i == 1, tmem, smem);
         }
         if (ok && j + 1 < nx[x]) score(leads, x, j + 1, tmem, smem);
       }
@@ -420,8 +425,11 @@ struct ApBlock {
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kHeld - 4 + e]);
         return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       };
+      const bool one = short_[x] && j + 1 == steps[x];  // (the same for all of the tile)
       float top = take(0);
-      if constexpr (Gm::kTwice) top = fmaxf(top, take(64));
+      if constexpr (Gm::kTwice) {
+        if (!one) top = fmaxf(top, take(64));
+      }
       const bool far = ref == -INFINITY ? top > -INFINITY : top - ref > slack;
       if (__any_sync(0xffffffffu, far)) {
         const float now = far ? top : ref;
@@ -458,7 +466,8 @@ struct ApBlock {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const int h = Gm::kTwice ? 1 - n : n, at = Gm::kTwice ? 0 : 64 * h;
-        if (Gm::kTwice && n == 1) take(0);
+        if (one && h == 1) continue;
+        if (Gm::kTwice && !one && n == 1) take(0);
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -484,27 +493,34 @@ struct ApBlock {
     }
     // rolled loops: this runs once, and unrolled it would wait for its instructions
 #pragma unroll 1
-    for (int i = 0; i < D; i += 32) {
-      float o[32];
-      tmem_ld32(to + i, o);
+    for (int i = 0; i < D; i += 64) {
+      float o[64];
+      tmem_ld64(to + i, o);
       uint8_t* at = q_at(x) + (i / 64) * Gm::kBlock + row * 128;
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
+      for (int e = 0; e < 64; e += 8) {
         uint4 v = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
                              pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
         if (steps[x] == 0) v = make_uint4(0u, 0u, 0u, 0u);  // O was never written
-        *reinterpret_cast<uint4*>(at + ((((i + e) % 64 / 8) ^ (row & 7)) << 4)) = v;
+        *reinterpret_cast<uint4*>(at + (((e / 8) ^ (row & 7)) << 4)) = v;
       }
     }
     __syncwarp();
     const long long mine = live ? ((static_cast<long long>(T.q0) + tok) * p.q_heads + head) * D : -1;
     constexpr int kLanes = D / 8;  // of a row
-#pragma unroll 4
-    for (int i = 0; i < kLanes; ++i) {
-      const int from = i * (32 / kLanes) + lane / kLanes, r = (row & ~31) + from, e = lane % kLanes;
-      const long long at = __shfl_sync(0xffffffffu, mine, from);
-      const uint4 v = *reinterpret_cast<const uint4*>(q_at(x) + (e / 8) * Gm::kBlock + r * 128 + (((e % 8) ^ (r & 7)) << 4));
-      if (at >= 0) *reinterpret_cast<uint4*>(p.out + at + 8 * e) = v;
+#pragma unroll 1
+    for (int i = 0; i < kLanes; i += 4) {
+      long long at[4];
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int from = (i + u) * (32 / kLanes) + lane / kLanes, r = (row & ~31) + from, e = lane % kLanes;
+        at[u] = __shfl_sync(0xffffffffu, mine, from);
+        v[u] = *reinterpret_cast<const uint4*>(q_at(x) + (e / 8) * Gm::kBlock + r * 128 + (((e % 8) ^ (r & 7)) << 4));
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (at[u] >= 0) *reinterpret_cast<uint4*>(p.out + at[u] + 8 * (lane % kLanes)) = v[u];
     }
     tc_fence_before();
   }
@@ -520,21 +536,8 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
     const CUtensorMap* map = threadIdx.x == 0 ? &p.tm_q : threadIdx.x == 1 ? &p.tm_k : &p.tm_v;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
-  grid_launch_dependents();
-  grid_dependency_wait();
   uint8_t* base = ap_smem + ((1024u - (smem_u32(ap_smem) & 1023u)) & 1023u);
-  ApBlock<D, X> B{p, base, reinterpret_cast<ApBars*>(base + Gm::kBars)};
-  if (!ap_find(p, p.units - 1 - static_cast<int>(blockIdx.x / p.kv_heads), X * p.tile_tokens, B.T)) return;
-  B.kvh = blockIdx.x % p.kv_heads;
-  bool some = false;
-#pragma unroll
-  for (int x = 0; x < X; ++x) {
-    const int t0 = B.T.first + x * p.tile_tokens, last = min(B.T.nq, t0 + p.tile_tokens) - 1;
-    const int keys = t0 < B.T.nq ? max(0, last + B.T.nk - B.T.nq + 1) : 0;
-    B.steps[x] = (keys + kApKeys - 1) / kApKeys;
-    some |= keys > 0;
-  }
-  ApBars* bar = B.bar;
+  ApBars* bar = reinterpret_cast<ApBars*>(base + Gm::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < X; ++i) {
@@ -554,6 +557,20 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
     bar->abort_flag = 0;
     mbar_init_fence();
   }
+  grid_launch_dependents();
+  grid_dependency_wait();
+  ApBlock<D, X> B{p, base, bar};
+  const bool work = ap_find(p, p.units - 1 - static_cast<int>(blockIdx.x / p.kv_heads), X * p.tile_tokens, B.T);
+  B.kvh = blockIdx.x % p.kv_heads;
+  bool some = false;
+#pragma unroll
+  for (int x = 0; x < X; ++x) {
+    const int t0 = B.T.first + x * p.tile_tokens, last = min(B.T.nq, t0 + p.tile_tokens) - 1;
+    const int keys = work && t0 < B.T.nq ? max(0, last + B.T.nk - B.T.nq + 1) : 0;
+    B.steps[x] = (keys + kApKeys - 1) / kApKeys;
+    B.short_[x] = keys > 0 && (keys - 1) % kApKeys < kApKeys / 2;
+    some |= keys > 0;
+  }
   if (warp == Gm::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar->tmem)), "r"(Gm::kTmem)
                  : "memory");
@@ -565,7 +582,7 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
   const uint32_t tmem = bar->tmem;
   if (warp < 4 * X) {
     if constexpr (X == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    B.soften(warp >> 2, tmem);
+    if (work) B.soften(warp >> 2, tmem);
   } else {
     if constexpr (X == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (some) {
