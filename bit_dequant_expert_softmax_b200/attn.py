@@ -32,6 +32,8 @@ class fmoe_attn_config(ctypes.Structure):
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_tokens: int = 64):
         super().__init__(q_heads, kv_heads, head_dim, page_tokens)
         self.ref = ctypes.byref(self)
+        self.heads = (q_heads, kv_heads, head_dim)  # (a field of the structure takes longer to read)
+        self.page_bytes = fmoe_kv_page_bytes(self)
 
 
 _lib = None
@@ -55,56 +57,38 @@ def lib():
     return _lib
 
 
-def _stream(stream, t) -> int:
-    """The raw stream handle to launch on; the tensors' device has to be the current one.
-    (torch.cuda.current_stream() takes 3 us, as long as a small call's launch.)"""
-    d = t.get_device()
-    if d != torch._C._cuda_getDevice():
-        _refuse(f"the tensors are on device {d}, which is not the current one")
-    return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
-
-
 def _refuse(what: str):
     raise fmoe.FmoeError(1, what)
 
 
-def _rows(t, heads: int, dim: int, what: str):
-    """(pointer, row stride, rows) of a bf16 [rows][heads][dim] tensor whose heads are contiguous."""
-    shape, stride = t.shape, t.stride()
-    if (t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != dim or stride[2] != 1
-            or (stride[1] != dim and heads > 1) or not t.is_cuda):
-        _refuse(f"{what}: bf16 [rows][{heads}][{dim}] with contiguous heads on the GPU is wanted")
-    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim, shape[0]
+# The checks below are written out per function and look at each property once: a small call's
+# launch takes 2 us, as much as twenty of them.
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
-def _whole(t, heads: int, dim: int, what: str):
-    p, stride, n = _rows(t, heads, dim, what)
-    if stride != heads * dim:
-        _refuse(f"{what}: contiguous rows are wanted")
-    return p, n
+def _stream(stream, device: int) -> int:
+    """The raw stream handle to launch on; the tensors' device has to be the current one.
+    (torch.cuda.current_stream() takes 3 us.)"""
+    if device < 0 or device != torch._C._cuda_getDevice():
+        _refuse(f"the tensors are not on the current CUDA device (theirs: {device})")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _ints(t, dtype, shape, what: str):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        _refuse(f"{what}: contiguous {dtype} {tuple(shape)} on the GPU is wanted")
-    return t.data_ptr()
+def _pages(cfg, cache) -> int:
+    """Page count of a cache tensor: uint8, contiguous, whole pages."""
+    size = cfg.page_bytes
+    n = cache.numel()
+    if not size or n % size or cache.dtype is not _U8 or not cache.is_contiguous():
+        _refuse(f"cache: contiguous uint8 pages of {size} bytes are wanted")
+    return n // size
 
 
-def _error(t):
+def _error(t, device: int):
     if t is None:
         return None
-    if t.element_size() != 4 or t.numel() != 1 or not t.is_cuda:
-        _refuse("error: one 32-bit word on the GPU is wanted")
+    if t.element_size() != 4 or t.numel() != 1 or t.get_device() != device:
+        _refuse("error: one 32-bit word on the same GPU is wanted")
     return t.data_ptr()
-
-
-def _pages(cfg, cache):
-    """Pointer and page count of a cache tensor: uint8, contiguous, whole pages."""
-    size = cfg.page_bytes = getattr(cfg, "page_bytes", None) or fmoe_kv_page_bytes(cfg)
-    n = cache.numel()
-    if cache.dtype is not torch.uint8 or not cache.is_contiguous() or not size or n % size or not cache.is_cuda:
-        _refuse(f"cache: contiguous uint8 pages of {size} bytes on the GPU are wanted")
-    return cache.data_ptr(), n // size
 
 
 def fmoe_kv_page_bytes(cfg: fmoe_attn_config) -> int:
@@ -138,83 +122,129 @@ def fmoe_kv_append(cfg: fmoe_attn_config, q, k, v, rope, positions, slots, cache
     """Rotates q and k [T][heads][D], writes k and v into the cache's slots, the rotated q and
     k to q_out and k_out.  rope fp32 [positions][2][rotary/2] or None (no rotation); q and
     q_out may be None together, k_out may be None."""
-    D, H, KV = cfg.head_dim, cfg.q_heads, cfg.kv_heads
-    kp, ks, T = _rows(k, KV, D, "k")
-    vp, vs, n = _rows(v, KV, D, "v")
-    qp, qs = None, 0
-    qo = ko = pos = table = None
-    known = rotary = 0
+    H, KV, D = cfg.heads
+    dev = cache.get_device()
+    T, kv, d = shape = k.shape
+    ks, k1, k2 = k.stride()
+    vs, v1, v2 = v.stride()
+    if (k.dtype is not _BF16 or v.dtype is not _BF16 or kv != KV or d != D or v.shape != shape or k2 != 1 or v2 != 1
+            or (KV > 1 and (k1 != D or v1 != D)) or k.get_device() != dev or v.get_device() != dev):
+        _refuse(f"k and v: bf16 [T][{KV}][{D}] with contiguous heads are wanted, on the cache's GPU")
+    if slots.dtype is not _I64 or slots.shape != (T,) or not slots.is_contiguous() or slots.get_device() != dev:
+        _refuse("slots: contiguous int64 [T] on the cache's GPU is wanted")
+    qp = qo = ko = pos = table = None
+    qs = known = rotary = 0
     if q is not None:
-        qp, qs, m = _rows(q, H, D, "q")
-        n = n if m == T else -1
+        n, h, d = q.shape
+        qs, q1, q2 = q.stride()
+        if q.dtype is not _BF16 or n != T or h != H or d != D or q2 != 1 or (H > 1 and q1 != D) or q.get_device() != dev:
+            _refuse(f"q: bf16 [T][{H}][{D}] with contiguous heads is wanted, on the cache's GPU")
+        qp = q.data_ptr()
     if q_out is not None:
-        qo, m = _whole(q_out, H, D, "q_out")
-        n = n if m == T else -1
+        if q_out.dtype is not _BF16 or q_out.shape != (T, H, D) or not q_out.is_contiguous() or q_out.get_device() != dev:
+            _refuse(f"q_out: contiguous bf16 [T][{H}][{D}] on the cache's GPU is wanted")
+        qo = q_out.data_ptr()
     if k_out is not None:
-        ko, m = _whole(k_out, KV, D, "k_out")
-        n = n if m == T else -1
-    if n != T:
-        _refuse("q, k, v, q_out and k_out have as many rows as each other")
+        if k_out.dtype is not _BF16 or k_out.shape != shape or not k_out.is_contiguous() or k_out.get_device() != dev:
+            _refuse(f"k_out: contiguous bf16 [T][{KV}][{D}] on the cache's GPU is wanted")
+        ko = k_out.data_ptr()
     if rope is not None:
         known, two, rotary = rope.shape
         rotary *= 2
-        if rope.dtype is not torch.float32 or two != 2 or not rope.is_contiguous() or not rope.is_cuda:
-            _refuse("rope: contiguous fp32 [positions][2][rotary/2] on the GPU is wanted")
-        table = rope.data_ptr()
-        pos = _ints(positions, torch.int32, (T,), "positions")
-    cp, pages = _pages(cfg, cache)
-    st = lib().fmoe_kv_append(cfg.ref, qp, qs, kp, ks, vp, vs, T, table, known, rotary, pos,
-                              _ints(slots, torch.int64, (T,), "slots"), cp, pages, qo, ko, _error(error),
-                              _stream(stream, cache))
-    fmoe._check(st, "fmoe_kv_append")
+        if rope.dtype is not _F32 or two != 2 or not rope.is_contiguous() or rope.get_device() != dev:
+            _refuse("rope: contiguous fp32 [positions][2][rotary/2] on the cache's GPU is wanted")
+        if (positions.dtype is not _I32 or positions.shape != (T,) or not positions.is_contiguous()
+                or positions.get_device() != dev):
+            _refuse("positions: contiguous int32 [T] on the cache's GPU is wanted")
+        table, pos = rope.data_ptr(), positions.data_ptr()
+    if T == 1:  # a single row's stride says nothing
+        qs, ks, vs = H * D, KV * D, KV * D
+    st = (_lib or lib()).fmoe_kv_append(cfg.ref, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, T, table, known, rotary, pos,
+                                        slots.data_ptr(), cache.data_ptr(), _pages(cfg, cache), qo, ko,
+                                        _error(error, dev), _stream(stream, dev))
+    if st:
+        fmoe._check(st, "fmoe_kv_append")
 
 
 def fmoe_kv_gather(cfg: fmoe_attn_config, cache, page_table, cu, k_out, v_out, first=None, error=None, stream=None):
     """Cached tokens as packed bf16 rows [rows][kv_heads][D]: sequence s's tokens from first[s]
     (0 without `first`) on into rows cu[s] .. cu[s+1] - 1."""
-    D, KV = cfg.head_dim, cfg.kv_heads
-    kp, n = _whole(k_out, KV, D, "k_out")
-    vp, m = _whole(v_out, KV, D, "v_out")
-    if n != m:
-        _refuse("k_out and v_out have as many rows as each other")
+    _, KV, D = cfg.heads
+    dev = cache.get_device()
+    n, kv, d = shape = k_out.shape
+    if (k_out.dtype is not _BF16 or v_out.dtype is not _BF16 or kv != KV or d != D or v_out.shape != shape
+            or not k_out.is_contiguous() or not v_out.is_contiguous() or k_out.get_device() != dev
+            or v_out.get_device() != dev):
+        _refuse(f"k_out and v_out: contiguous bf16 [rows][{KV}][{D}] on the cache's GPU are wanted")
     seqs, width = page_table.shape
-    cp, pages = _pages(cfg, cache)
-    st = lib().fmoe_kv_gather(cfg.ref, cp, pages, _ints(page_table, torch.int32, (seqs, width), "page_table"), width, seqs,
-                              None if first is None else _ints(first, torch.int32, (seqs,), "first"),
-                              _ints(cu, torch.int32, (seqs + 1,), "cu"), n, kp, vp, _error(error), _stream(stream, cache))
-    fmoe._check(st, "fmoe_kv_gather")
+    if (page_table.dtype is not _I32 or cu.dtype is not _I32 or cu.shape != (seqs + 1,) or not page_table.is_contiguous()
+            or not cu.is_contiguous() or page_table.get_device() != dev or cu.get_device() != dev):
+        _refuse("page_table and cu: contiguous int32 [seqs][width] and [seqs + 1] on the cache's GPU are wanted")
+    fp = None
+    if first is not None:
+        if first.dtype is not _I32 or first.shape != (seqs,) or not first.is_contiguous() or first.get_device() != dev:
+            _refuse("first: contiguous int32 [seqs] on the cache's GPU is wanted")
+        fp = first.data_ptr()
+    st = (_lib or lib()).fmoe_kv_gather(cfg.ref, cache.data_ptr(), _pages(cfg, cache), page_table.data_ptr(), width, seqs, fp,
+                                        cu.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(), _error(error, dev),
+                                        _stream(stream, dev))
+    if st:
+        fmoe._check(st, "fmoe_kv_gather")
 
 
 def fmoe_attn_decode(cfg: fmoe_attn_config, q, cache, page_table, lens, out, scale, workspace, error=None, stream=None):
     """out[s] = attention of the single query row q[s] [q_heads][D] over the first lens[s]
     cached tokens of the sequence."""
-    D, H = cfg.head_dim, cfg.q_heads
-    qp, qs, seqs = _rows(q, H, D, "q")
-    op, n = _whole(out, H, D, "out")
-    width = page_table.shape[-1]
-    if n != seqs or workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or not workspace.is_cuda:
-        _refuse("q and out have as many rows as each other; workspace: contiguous uint8 on the GPU is wanted")
-    cp, pages = _pages(cfg, cache)
-    st = lib().fmoe_attn_decode(cfg.ref, qp, qs, cp, pages, _ints(page_table, torch.int32, (seqs, width), "page_table"),
-                                width, _ints(lens, torch.int32, (seqs,), "lens"), seqs, scale, op, workspace.data_ptr(),
-                                workspace.numel(), _error(error), _stream(stream, q))
-    fmoe._check(st, "fmoe_attn_decode")
+    H, _, D = cfg.heads
+    dev = cache.get_device()
+    seqs, h, d = shape = q.shape
+    qs, q1, q2 = q.stride()
+    if (q.dtype is not _BF16 or out.dtype is not _BF16 or h != H or d != D or q2 != 1 or (H > 1 and q1 != D)
+            or out.shape != shape or not out.is_contiguous() or q.get_device() != dev or out.get_device() != dev):
+        _refuse(f"q and out: bf16 [seqs][{H}][{D}] on the cache's GPU are wanted, contiguous but for q's rows")
+    rows, width = page_table.shape
+    if (page_table.dtype is not _I32 or lens.dtype is not _I32 or rows != seqs or lens.shape != (seqs,)
+            or not page_table.is_contiguous() or not lens.is_contiguous() or page_table.get_device() != dev
+            or lens.get_device() != dev):
+        _refuse("page_table and lens: contiguous int32 [seqs][width] and [seqs] on the cache's GPU are wanted")
+    if workspace.dtype is not _U8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        _refuse("workspace: contiguous uint8 on the cache's GPU is wanted")
+    st = (_lib or lib()).fmoe_attn_decode(cfg.ref, q.data_ptr(), qs if seqs > 1 else H * D, cache.data_ptr(),
+                                          _pages(cfg, cache), page_table.data_ptr(), width, lens.data_ptr(), seqs, scale,
+                                          out.data_ptr(), workspace.data_ptr(), workspace.numel(), _error(error, dev),
+                                          _stream(stream, dev))
+    if st:
+        fmoe._check(st, "fmoe_attn_decode")
     return out
 
 
 def fmoe_attn_prompt(cfg: fmoe_attn_config, q, k, v, cu_q, cu_k, out, scale, error=None, stream=None):
     """Causal attention of packed sequences: q and out [q_rows][q_heads][D], k and v
     [k_rows][kv_heads][D], row offsets cu_q and cu_k int32 [seqs + 1]."""
-    D, H, KV = cfg.head_dim, cfg.q_heads, cfg.kv_heads
-    qp, qs, n = _rows(q, H, D, "q")
-    kp, ks, m = _rows(k, KV, D, "k")
-    vp, vs, mv = _rows(v, KV, D, "v")
-    op, no = _whole(out, H, D, "out")
-    seqs = cu_q.shape[0] - 1
-    if mv != m or no != n:
-        _refuse("k and v, and q and out, have as many rows as each other")
-    st = lib().fmoe_attn_prompt(cfg.ref, qp, qs, kp, ks, vp, vs, _ints(cu_q, torch.int32, (seqs + 1,), "cu_q"),
-                                _ints(cu_k, torch.int32, (seqs + 1,), "cu_k"), seqs, n, m, scale, op, _error(error),
-                                _stream(stream, q))
-    fmoe._check(st, "fmoe_attn_prompt")
+    H, KV, D = cfg.heads
+    dev = q.get_device()
+    n, h, d = shape = q.shape
+    qs, q1, q2 = q.stride()
+    if (q.dtype is not _BF16 or out.dtype is not _BF16 or h != H or d != D or q2 != 1 or (H > 1 and q1 != D)
+            or out.shape != shape or not out.is_contiguous() or out.get_device() != dev):
+        _refuse(f"q and out: bf16 [q_rows][{H}][{D}] on one GPU are wanted, contiguous but for q's rows")
+    m, kv, d = shape = k.shape
+    ks, k1, k2 = k.stride()
+    vs, v1, v2 = v.stride()
+    if (k.dtype is not _BF16 or v.dtype is not _BF16 or kv != KV or d != D or v.shape != shape or k2 != 1 or v2 != 1
+            or (KV > 1 and (k1 != D or v1 != D)) or k.get_device() != dev or v.get_device() != dev):
+        _refuse(f"k and v: bf16 [k_rows][{KV}][{D}] with contiguous heads are wanted, on q's GPU")
+    ends = cu_q.numel()
+    if (cu_q.dtype is not _I32 or cu_k.dtype is not _I32 or ends < 1 or cu_k.numel() != ends or not cu_q.is_contiguous()
+            or not cu_k.is_contiguous() or cu_q.get_device() != dev or cu_k.get_device() != dev):
+        _refuse("cu_q and cu_k: contiguous int32 [seqs + 1] on q's GPU are wanted")
+    if n <= 1:  # a single row's stride says nothing
+        qs = H * D
+    if m <= 1:
+        ks = vs = KV * D
+    st = (_lib or lib()).fmoe_attn_prompt(cfg.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu_q.data_ptr(),
+                                          cu_k.data_ptr(), ends - 1, n, m, scale, out.data_ptr(), _error(error, dev),
+                                          _stream(stream, dev))
+    if st:
+        fmoe._check(st, "fmoe_attn_prompt")
     return out
