@@ -148,7 +148,10 @@ struct AdGeom {
   static constexpr int kWarp = kRing + kState;                // its ring and the part it began with
   static constexpr int kControl = kAdWarps * kWarp;
   static constexpr int kBars = kControl + kAdWarps * static_cast<int>(sizeof(AdControl));
-  static constexpr int kSmem = kBars + kAdWarps * kStages * 8;
+  // at least so much that no more than kBlocks blocks fit on an SM (228 KB with 1 KB per block): the
+  // grid has kBlocks per SM, and where one SM had room for more, others stayed empty
+  static constexpr int kNeeds = kBars + kAdWarps * kStages * 8, kFills = 228 * 1024 / (kBlocks + 1);
+  static constexpr int kSmem = kNeeds > kFills ? kNeeds : kFills;
   static_assert(kStages + 1 <= kAdParts, "parts in flight");
   static_assert(kState <= kRing, "the part that a warp ends with goes into its ring");
 };

@@ -244,89 +244,86 @@ struct KvGatherParams {
 };
 
 
-// `Rows` packed rows per block (blockIdx.x), heads over blockIdx.y.  The first threads find each
-// row's place in the cache (-1: none); then a lane group takes one head's keys or values of one
-// row, up to 8 of them in flight.
+// `Rows` packed rows per block (blockIdx.x), an eighth per warp, heads over blockIdx.y.  A warp
+// finds its rows' sequences by counting those that end at or before each row, a lane then its
+// row's place in the cache (-1: none); a lane group takes one head's keys or values of one
+// row, up to 8 of them in flight.  Codes become floats in place: the low bits of 2^23.
 template <int D, int Rows>
 __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const __grid_constant__ KvGatherParams p) {
   using Gm = KvGeom<D>;
-  constexpr int kPer = kKvThreads / Gm::kLanes;
-  __shared__ long long where[Rows];
-  __shared__ int seq_of[Rows];
+  constexpr int kMine = Rows / (kKvThreads / 32);     // rows of a warp
+  constexpr int kPer = 32 / Gm::kLanes;               // lane groups of a warp
   grid_launch_dependents();
   grid_dependency_wait();
-  const long long r0 = static_cast<long long>(blockIdx.x) * Rows;
-  if (threadIdx.x < Rows) seq_of[threadIdx.x] = -1;
-  __syncthreads();
-  // sequences mark the row that they begin at, or the first row if they began before it; a row's
-  // sequence is the last mark up to it
-  for (int s = threadIdx.x; s < p.seqs; s += kKvThreads) {
-    const long long a = max(r0, static_cast<long long>(__ldg(p.cu + s)));
-    if (a < r0 + Rows && a < __ldg(p.cu + s + 1)) atomicMax(&seq_of[a - r0], s);
-  }
-  __syncthreads();
-  if (threadIdx.x < (Rows + 31) / 32 * 32) {
-    const long long r = r0 + threadIdx.x;
-    int s = threadIdx.x < Rows ? seq_of[threadIdx.x] : -1;
+  const int tid = threadIdx.x & 31, lane = tid % Gm::kLanes, grp = tid / Gm::kLanes;
+  const long long r0 = static_cast<long long>(blockIdx.x) * Rows + threadIdx.x / 32 * kMine;
+  int ended = 0;  // of lane's row: sequences that end at or before it
+  for (int s0 = 0; s0 < p.seqs; s0 += 32) {
+    const int end = s0 + tid < p.seqs ? __ldg(p.cu + s0 + tid + 1) : INT32_MAX;
 #pragma unroll
-    for (int x = 1; x < 32; x *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, s, x);
-      if ((threadIdx.x & 31) >= x) s = max(s, y);
+    for (int i = 0; i < kMine; ++i) {
+      const int n = __popc(__ballot_sync(0xffffffffu, end <= r0 + i));
+      if (tid == i) ended += n;
     }
-    for (int w = threadIdx.x & ~31; w > 0; w -= 32) s = max(s, __reduce_max_sync(0xffffffffu, seq_of[w - 32 + (threadIdx.x & 31)]));
-    if (s >= 0 && r >= __ldg(p.cu + s + 1)) s = -1;
-    long long at = -1;
-    if (threadIdx.x < Rows && r < p.rows && s >= 0) {
-      const long long t0 = p.first != nullptr ? __ldg(p.first + s) : 0, t = t0 + (r - __ldg(p.cu + s));
-      const int index = static_cast<int>(div64(t, p.page_tokens));
-      if (t0 < 0 || index >= p.width) {
-        kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
+  }
+  long long at = -1;
+  if (tid < kMine && r0 + tid < p.rows && ended < p.seqs) {
+    const long long in = r0 + tid - __ldg(p.cu + ended), t0 = p.first != nullptr ? __ldg(p.first + ended) : 0, t = t0 + in;
+    const int index = in >= 0 && t >= 0 ? static_cast<int>(div64(t, p.page_tokens)) : 0;
+    if (in < 0 || t0 < 0 || index >= p.width) {
+      kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
+    } else {
+      const int page = __ldg(p.table + static_cast<long long>(ended) * p.width + index);
+      if (page < 0 || page >= p.pages) {
+        kv_error(p.err, FMOE_DEVERR_BAD_PAGE);
       } else {
-        const int page = __ldg(p.table + static_cast<long long>(s) * p.width + index);
-        if (page < 0 || page >= p.pages) {
-          kv_error(p.err, FMOE_DEVERR_BAD_PAGE);
-        } else {
-          const int place = static_cast<int>(t - static_cast<long long>(index) * p.page_tokens);
-          at = page * p.page_bytes + static_cast<long long>(place / kKvTile) * Gm::kTileBytes + place % kKvTile;
-        }
+        // page and tile offsets are multiples of 16: the row in the tile rides in the low bits
+        const int place = static_cast<int>(t - static_cast<long long>(index) * p.page_tokens);
+        at = page * p.page_bytes + static_cast<long long>(place / kKvTile) * Gm::kTileBytes + place % kKvTile;
       }
     }
-    if (threadIdx.x < Rows) where[threadIdx.x] = at;
   }
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && __ldg(p.cu + p.seqs) > p.rows)
     kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
-  __syncthreads();
-  const int lane = threadIdx.x % Gm::kLanes, grp = threadIdx.x / Gm::kLanes;
   const long long head_bytes = static_cast<long long>(p.page_tokens / kKvTile) * Gm::kTileBytes;
   for (int h = blockIdx.y; h < p.kv_heads; h += gridDim.y) {
-    constexpr int kTasks = 2 * Rows / kPer, kAhead = 8;
+    constexpr int kTasks = 2 * kMine / kPer, kAhead = kTasks < 8 ? kTasks : 8;
+    static_assert(kTasks % kAhead == 0, "tasks of a lane group");
 #pragma unroll
     for (int i0 = 0; i0 < kTasks; i0 += kAhead) {
       uint32_t w[kAhead], sb[kAhead];
+      bool is[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead && i0 + u < kTasks; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int i = (i0 + u) * kPer + grp, rr = i >> 1;
         const bool val = i & 1;
-        const long long at = where[rr];
+        const long long from = __shfl_sync(0xffffffffu, at, rr);
+        is[u] = from >= 0;
+        const int row = static_cast<int>(from & 15);
+        const uint8_t* tile = p.cache + (from - row) + h * head_bytes;
         w[u] = sb[u] = 0;
-        if (at < 0) continue;
-        // page and tile offsets are multiples of 16, the row in the tile rides in the low bits
-        const int row = static_cast<int>(at & 15);
-        const uint8_t* tile = p.cache + (at - row) + h * head_bytes;
-        w[u] = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffV : 0) + row * Gm::kRow) + (lane & 7) * Gm::kGroups + lane / 8);
-        sb[u] = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffVs : Gm::kOffKs)) + row * Gm::kGroups + lane / 8);
+        if (is[u]) {
+          w[u] = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffV : 0) + row * Gm::kRow) + (lane & 7) * Gm::kGroups + lane / 8);
+          sb[u] = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffVs : Gm::kOffKs)) + row * Gm::kGroups + lane / 8);
+        }
       }
 #pragma unroll
-      for (int u = 0; u < kAhead && i0 + u < kTasks; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int i = (i0 + u) * kPer + grp, rr = i >> 1;
-        if (where[rr] < 0) continue;
-        const float s = sb_scale(sb[u]), b = sb_bias(sb[u]);
-        uint32_t o[4];
+        const float b = sb_bias(sb[u]);
+        float x[8], s = sb_scale(sb[u]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          o[c] = pack_bf16(fmaf(s, static_cast<float>((w[u] >> (8 * c)) & 15u), b), fmaf(s, static_cast<float>((w[u] >> (8 * c + 4)) & 15u), b));
+        for (int c = 0; c < 4; ++c) {  // 16^c code times scale / 16^c: both exact, the sum is rounded once
+          constexpr uint32_t kBits = 0x4B000000u;  // 2^23
+          const uint32_t lo = w[u], hi = w[u] >> 16;
+          x[c] = fmaf(__uint_as_float((lo & (15u << (4 * c))) | kBits) - 0x1p23f, s, b);
+          x[c + 4] = fmaf(__uint_as_float((hi & (15u << (4 * c))) | kBits) - 0x1p23f, s, b);
+          s *= 0.0625f;
+        }
         uint16_t* dst = (i & 1 ? p.v_out : p.k_out) + ((r0 + rr) * p.kv_heads + h) * D + lane * 8;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (is[u])
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
       }
     }
   }
