@@ -26,6 +26,7 @@ EXPORTS = ["fmoe_kv_page_bytes", "fmoe_kv_append", "fmoe_kv_gather", "fmoe_attn_
 
 
 class fmoe_attn_config(ctypes.Structure):
+    """Geometry of one attention layer; not to be changed once made."""
     _fields_ = [("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("page_tokens", ctypes.c_int)]
 

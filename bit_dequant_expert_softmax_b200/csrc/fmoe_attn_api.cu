@@ -33,15 +33,15 @@ bool rows_ok(const void* p, int64_t stride, int heads, int D) {
   return p && on_boundary(p, 16) && stride >= (int64_t)heads * D && stride % 8 == 0;
 }
 
-// Whether an output of T contiguous rows meets an input's memory other than as the input
-// itself, row on row.
-bool crosses(const uint16_t* in, int64_t in_stride, const uint16_t* out, int64_t T, int heads, int D) {
-  if (!in || !out || T < 1) return false;
-  const int64_t row = (int64_t)heads * D;
-  const uint16_t *in_end = in + (T - 1) * in_stride + row, *out_end = out + T * row;
-  if (out_end <= in || in_end <= out) return false;
-  return !(out == in && (in_stride == row || T == 1));
-}
+// Rows of bf16 in memory: `rows` of them, `stride` elements apart, `width` elements each.
+struct Span {
+  const uint16_t* at;
+  int64_t rows, stride, width;
+  const uint16_t* end() const { return at + (rows - 1) * stride + width; }
+};
+bool meet(const Span& a, const Span& b) { return a.at && b.at && a.rows > 0 && b.rows > 0 && a.at < b.end() && b.at < a.end(); }
+// The same rows in the same places.
+bool alike(const Span& a, const Span& b) { return a.at == b.at && a.width == b.width && (a.stride == b.stride || a.rows == 1); }
 
 template <class P>
 fmoe_status launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
@@ -186,7 +186,11 @@ fmoe_status fmoe_kv_append(const fmoe_attn_config* c, const uint16_t* q, int64_t
   if (rotary && (!rope || !on_boundary(rope, 16) || !positions || !on_boundary(positions, 4) || rope_positions < 1))
     return FMOE_ERR_INVALID_ARG;
   if (!on_boundary(q_out, 16) || !on_boundary(k_out, 16) || !on_boundary(device_error, 4)) return FMOE_ERR_INVALID_ARG;
-  if (crosses(q, q_stride, q_out, T, c->q_heads, D) || crosses(k, k_stride, k_out, T, c->kv_heads, D))
+  const int64_t wide = (int64_t)c->q_heads * D, narrow = (int64_t)c->kv_heads * D;
+  const Span sq{q, T, q_stride, wide}, sk{k, T, k_stride, narrow}, sv{v, T, v_stride, narrow};
+  const Span oq{q_out, T, wide, wide}, ok{k_out, T, narrow, narrow};
+  if ((meet(oq, sq) && !alike(oq, sq)) || (meet(ok, sk) && !alike(ok, sk)) || meet(oq, sk) || meet(oq, sv) ||
+      meet(ok, sq) || meet(ok, sv) || meet(oq, ok))
     return FMOE_ERR_INVALID_ARG;
   KvAppendParams p{};
   p.q = q, p.k = k, p.v = v;
@@ -224,6 +228,8 @@ fmoe_status fmoe_kv_gather(const fmoe_attn_config* c, const void* cache, int64_t
       !on_boundary(first, 4) || !k_out || !on_boundary(k_out, 16) || !v_out || !on_boundary(v_out, 16) ||
       !on_boundary(device_error, 4))
     return FMOE_ERR_INVALID_ARG;
+  const int64_t narrow = (int64_t)c->kv_heads * c->head_dim;
+  if (meet(Span{k_out, rows, narrow, narrow}, Span{v_out, rows, narrow, narrow})) return FMOE_ERR_INVALID_ARG;
   KvGatherParams p{};
   p.cache = static_cast<const uint8_t*>(cache);
   p.pages = pages, p.page_bytes = kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens), p.rows = rows;
@@ -247,6 +253,8 @@ fmoe_status fmoe_attn_decode(const fmoe_attn_config* c, const uint16_t* q, int64
       !on_boundary(page_table, 4) || !lens || !on_boundary(lens, 4) || !out || !on_boundary(out, 16) ||
       !on_boundary(device_error, 4))
     return FMOE_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)c->q_heads * D;
+  if (meet(Span{out, seqs, row, row}, Span{q, seqs, q_stride, row})) return FMOE_ERR_INVALID_ARG;
   const AdWorkspace w = decode_workspace(D);
   if (!workspace || workspace_bytes < w.size) return FMOE_ERR_NO_WORKSPACE;
   if (!on_boundary(workspace, 256)) return FMOE_ERR_INVALID_ARG;
@@ -292,6 +300,11 @@ fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64
       !on_boundary(out, 16) || !on_boundary(device_error, 4))
     return FMOE_ERR_INVALID_ARG;
   if (!rows_ok(k, k_stride, c->kv_heads, D) || !rows_ok(v, v_stride, c->kv_heads, D)) return FMOE_ERR_INVALID_ARG;
+  const int64_t wide = (int64_t)c->q_heads * D, narrow = (int64_t)c->kv_heads * D;
+  const Span so{out, q_rows, wide, wide};
+  if (meet(so, Span{q, q_rows, q_stride, wide}) || meet(so, Span{k, k_rows, k_stride, narrow}) ||
+      meet(so, Span{v, k_rows, v_stride, narrow}))
+    return FMOE_ERR_INVALID_ARG;
   const int G = c->q_heads / c->kv_heads;
   ApParams p{};
   p.tile_tokens = kApRows / G;

@@ -84,8 +84,8 @@ size_t fmoe_kv_page_bytes(const fmoe_attn_config* cfg);
  *   q_out    bf16 [T][q_heads][D], k_out bf16 [T][kv_heads][D] (may be NULL): the rotated q
  *            and k.  q_out may be q itself (and k_out k) when its stride is that of q_out;
  *            no other overlap of inputs and outputs is allowed.
- * A token with a negative slot is padding: nothing of it is read or written.  A slot or
- * position out of range sets its bit and the token is left out likewise.  T == 0 is a
+ * A token with a negative slot is padding: nothing is written for it.  A slot or position out
+ * of range sets its bit and the token is left out likewise.  T == 0 is a
  * no-op.  Errors: INVALID_ARG, UNSUPPORTED (head_dim other than 64 and 128), CUDA. */
 fmoe_status fmoe_kv_append(const fmoe_attn_config* cfg, const uint16_t* q, int64_t q_stride, const uint16_t* k,
                            int64_t k_stride, const uint16_t* v, int64_t v_stride, int T, const float* rope,
@@ -95,7 +95,7 @@ fmoe_status fmoe_kv_append(const fmoe_attn_config* cfg, const uint16_t* q, int64
 
 /* Cached tokens back as bf16(scale * code + bias), packed: for sequence s the tokens
  * first[s] .. first[s] + cu[s+1] - cu[s] - 1 go to rows cu[s] .. cu[s+1] - 1 of k_out and
- * v_out, bf16 [rows][kv_heads][D], 16-byte aligned (the keys and values that
+ * v_out, bf16 [rows][kv_heads][D], 16-byte aligned, apart (the keys and values that
  * fmoe_attn_prompt takes where a prompt continues a cached prefix).  page_table int32
  * [seqs][table_width]; first int32 [seqs], or NULL for zeros; cu int32 [seqs + 1],
  * cu[0] = 0, not decreasing.  Rows from cu[seqs] on are left as they were; cu beyond `rows`
@@ -112,10 +112,14 @@ fmoe_status fmoe_kv_gather(const fmoe_attn_config* cfg, const void* cache, int64
  * over the cached (dequantised) keys and values, rounded once to bf16.  lens[s] <= 0 gives
  * zeros.  q bf16 [seqs] rows q_stride elements apart (heads contiguous), 16-byte aligned,
  * stride a multiple of 8; out bf16 [seqs][q_heads][D], 16-byte aligned; page_table int32
- * [seqs][table_width] (entries behind a sequence's length are not read); lens int32 [seqs].
+ * [seqs][table_width] (entries behind a sequence's length are not used); lens int32 [seqs];
+ * table_width * P at most 2^30.  out does not overlap q.
  * A length beyond table_width * P is cut to it (and its bit set); the keys of a bad page
  * are left out (and its bit set).  A NaN or infinity in a cached key or value reaches the
  * outputs of its own sequence and key/value head only.
+ * Range: |q| and the cached scales below 2^60 and |scale| below 2^48 (codes enter the products
+ * as multiples of 2^-133 and the other operands carry 2^60 against them); queries below 2^-50
+ * lose bits.
  *
  * workspace: fmoe_attn_workspace_bytes() bytes, 256-byte aligned, zeroed by the caller
  * before its first use; every call leaves it ready for the next, whatever its sizes and

@@ -81,7 +81,7 @@ def test_append_refusals(attn):
                 dict(err=A + 2),
                 dict(qs=768, qo=A),        # in place with another stride
                 dict(qo=A + 1024),         # one token further on in the input
-                dict(ko=A + 16)):
+                dict(ko=A + 16), dict(qo=B + 64, ko=B + 128), dict(v=B, vs=256)):
         assert _call(f, names, good, **bad) == 1, bad
 
 
@@ -93,7 +93,7 @@ def test_gather_refusals(attn):
     assert _call(f, names, good, seqs=0) == 0 and _call(f, names, good, rows=0) == 0
     for bad in (dict(cfg=None), dict(cache=None), dict(cache=A + 16), dict(pages=-1), dict(table=None), dict(width=0),
                 dict(seqs=-1), dict(first=A + 1), dict(cu=None), dict(rows=-1), dict(rows=1 << 31), dict(ko=None),
-                dict(vo=B + 8), dict(err=A + 1)):
+                dict(vo=B + 8), dict(vo=B + 1024), dict(err=A + 1)):
         assert _call(f, names, good, **bad) == 1, bad
 
 
@@ -107,7 +107,8 @@ def test_decode_refusals(attn):
     assert _call(f, names, good, ws=None) == 4 and _call(f, names, good, bytes=size - 1) == 4
     for bad in (dict(cfg=None), dict(q=None), dict(q=A + 8), dict(qs=500), dict(cache=None), dict(pages=-1),
                 dict(table=None), dict(width=0), dict(width=1 << 25), dict(lens=None), dict(seqs=-1),
-                dict(scale=float("nan")), dict(out=None), dict(out=B + 8), dict(ws=B + 128), dict(err=A + 2)):
+                dict(scale=float("nan")), dict(out=None), dict(out=B + 8), dict(out=A + 1024), dict(ws=B + 128),
+                dict(err=A + 2)):
         assert _call(f, names, good, **bad) == 1, bad
 
 
@@ -119,7 +120,8 @@ def test_prompt_refusals(attn):
     assert _call(f, names, good, seqs=0) == 0 and _call(f, names, good, n=0) == 0
     for bad in (dict(cfg=None), dict(q=None), dict(q=A + 4), dict(qs=248), dict(k=None), dict(ks=132), dict(v=None),
                 dict(vs=64), dict(cq=None), dict(ck=None), dict(seqs=-1), dict(n=-1), dict(m=-1), dict(n=1 << 31),
-                dict(scale=float("nan")), dict(out=None), dict(out=B + 8), dict(err=A + 3)):
+                dict(scale=float("nan")), dict(out=None), dict(out=B + 8), dict(out=A), dict(err=A + 3),
+                dict(v=B + 4096, vs=128)):
         assert _call(f, names, good, **bad) == 1, bad
 
 

@@ -341,6 +341,26 @@ def test_decode_far_pages(attn):
         assert np.array_equal(_f32(got), ao.bf16_round(want))
 
 
+def test_decode_two_streams_at_once(attn):
+    """Calls on two streams at the same time, each with its own workspace."""
+    rng = np.random.default_rng(14)
+    cfg = attn.fmoe_attn_config(32, 8, 128, 64)
+    cache = _filled(attn, cfg, 64, 4)
+    jobs = []
+    for i in range(2):
+        lens = [900 + 100 * i, 0, 64, 333]
+        table = _table(rng, lens, 64, 64)
+        jobs.append((lens, table, _bf16(rng, 4, 32, 128), attn.attn_workspace(cfg), torch.cuda.Stream(), _i32(table), _i32(lens),
+                     torch.empty(4, 32, 128, dtype=torch.bfloat16, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for lens, _, q, ws, stream, t, n, out in jobs:
+            attn.fmoe_attn_decode(cfg, q, cache, t, n, out, 0.1, ws, stream=stream)
+    torch.cuda.synchronize()
+    for lens, table, q, _, _, _, _, out in jobs:
+        _check_decode(cfg, q, cache, table, lens, 0.1, out)
+
+
 def test_decode_streams_and_graph(attn):
     """On another stream; captured once and replayed after the lengths and the cache changed;
     the same workspace with other sizes in between."""
@@ -392,7 +412,13 @@ def _check_prompt(q, k, v, cq, ck, scale, out):
 @pytest.mark.parametrize("H,KV,D,lq,more", [
     (4, 2, 128, [1], [0]), (8, 8, 64, [127, 1, 0, 129], None), (32, 8, 128, [333], [0]),
     (40, 8, 64, [20, 300, 7], [100, 0, 513]), (6, 2, 128, [64, 65], [-30, 3]), (14, 2, 64, [50, 40], [-60, -40]),
-    (128, 1, 64, [3, 40], [5, 0]), (33, 1, 128, [77], [200]), (24, 3, 128, [700, 513], [0, 1]), (1, 1, 64, [1500], [0])])
+    (128, 1, 64, [3, 40], [5, 0]), (33, 1, 128, [77], [200]), (24, 3, 128, [700, 513], [0, 1]), (1, 1, 64, [1500], [0]),
+    # lengths around the steps of 64 and 128 keys
+    (4, 1, 128, [63, 64, 65, 127, 128, 129, 191, 192, 193, 256, 257, 2], None),
+    (7, 1, 64, [63, 64, 65, 127, 128, 129, 191, 192, 193], [1, 64, 0, 65, 128, 0, 63, 1, 2]),
+    # long sequences and blocks for every SM: two row tiles per block
+    (32, 8, 128, [1400], [0]), (40, 8, 64, [1300, 40], [300, -40]), (16, 16, 64, [2600], [-100]),
+    (28, 4, 128, [1200, 900, 31], [0, 130, 2])])
 def test_prompt(attn, H, KV, D, lq, more):
     rng = np.random.default_rng(H + sum(lq))
     cfg = attn.fmoe_attn_config(H, KV, D)
