@@ -16,7 +16,7 @@ namespace {
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int kMaxGridY = 65535;
 constexpr int kFewTokens = 480;  // fmoe_kv_append: 300 tokens of 32 + 2 x 4 heads take 6.3 us by blocks, 8.1 by warps; 600: 9.8, 8.5
-constexpr int kGatherWide = 400;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 5.5 us 64 rows a block, 4.8 us 16; 4000: 6.9, 7.6
+constexpr int kGatherWide = 400;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 5.9 us 64 rows a block, 5.0 us 16; 4000: 7.0, 8.0
 
 bool on_boundary(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 

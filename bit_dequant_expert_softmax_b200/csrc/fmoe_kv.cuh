@@ -234,6 +234,16 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
   }
 }
 
+template <int N>
+__device__ __forceinline__ void load_nc(uint32_t (&w)[N], const uint8_t* src) {
+  if constexpr (N == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+  }
+}
+
 struct KvGatherParams {
   const uint8_t* cache;
   long long pages, page_bytes, rows;
@@ -246,16 +256,18 @@ struct KvGatherParams {
 
 // `Rows` packed rows per block (blockIdx.x), an eighth per warp, heads over blockIdx.y.  A warp
 // finds its rows' sequences by counting those that end at or before each row, a lane then its
-// row's place in the cache (-1: none); a lane group takes one head's keys or values of one
-// row, up to 8 of them in flight.  Codes become floats in place: the low bits of 2^23.
+// row's place in the cache (-1: none); eight lanes take one head's keys or values of one row, a
+// lane the same 8-channel block of every 64-channel group (one load of codes; the stores of a
+// group's blocks join to 128 bytes), several of them in flight.  Codes become floats in place,
+// as the low bits of 2^23.
 template <int D, int Rows>
 __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const __grid_constant__ KvGatherParams p) {
   using Gm = KvGeom<D>;
   constexpr int kMine = Rows / (kKvThreads / 32);     // rows of a warp
-  constexpr int kPer = 32 / Gm::kLanes;               // lane groups of a warp
+  constexpr int NG = Gm::kGroups;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int tid = threadIdx.x & 31, lane = tid % Gm::kLanes, grp = tid / Gm::kLanes;
+  const int tid = threadIdx.x & 31, lane = tid & 7, grp = tid >> 3;
   const long long r0 = static_cast<long long>(blockIdx.x) * Rows + threadIdx.x / 32 * kMine;
   int ended = 0;  // of lane's row: sequences that end at or before it
   for (int s0 = 0; s0 < p.seqs; s0 += 32) {
@@ -287,43 +299,46 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const __grid_cons
     kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
   const long long head_bytes = static_cast<long long>(p.page_tokens / kKvTile) * Gm::kTileBytes;
   for (int h = blockIdx.y; h < p.kv_heads; h += gridDim.y) {
-    constexpr int kTasks = 2 * kMine / kPer, kAhead = kTasks < 8 ? kTasks : 8;
-    static_assert(kTasks % kAhead == 0, "tasks of a lane group");
+    constexpr int kTasks = 2 * kMine / 4;  // of eight lanes
 #pragma unroll
-    for (int i0 = 0; i0 < kTasks; i0 += kAhead) {
-      uint32_t w[kAhead], sb[kAhead];
-      bool is[kAhead];
+    for (int u0 = 0; u0 < kTasks; u0 += 4) {
+      uint32_t w[4][NG], sb[4][NG];
+      bool is[4];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = (i0 + u) * kPer + grp, rr = i >> 1;
+      for (int u = 0; u < 4 && u0 + u < kTasks; ++u) {
+        const int i = (u0 + u) * 4 + grp, rr = i >> 1;
         const bool val = i & 1;
         const long long from = __shfl_sync(0xffffffffu, at, rr);
         is[u] = from >= 0;
         const int row = static_cast<int>(from & 15);
         const uint8_t* tile = p.cache + (from - row) + h * head_bytes;
-        w[u] = sb[u] = 0;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) w[u][g] = sb[u][g] = 0;
         if (is[u]) {
-          w[u] = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffV : 0) + row * Gm::kRow) + (lane & 7) * Gm::kGroups + lane / 8);
-          sb[u] = __ldg(reinterpret_cast<const uint32_t*>(tile + (val ? Gm::kOffVs : Gm::kOffKs)) + row * Gm::kGroups + lane / 8);
+          load_nc<NG>(w[u], tile + (val ? Gm::kOffV : 0) + row * Gm::kRow + lane * (4 * NG));
+          load_nc<NG>(sb[u], tile + (val ? Gm::kOffVs : Gm::kOffKs) + row * (4 * NG));
         }
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = (i0 + u) * kPer + grp, rr = i >> 1;
-        const float b = sb_bias(sb[u]);
-        float x[8], s = sb_scale(sb[u]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16^c code times scale / 16^c: both exact, the sum is rounded once
-          constexpr uint32_t kBits = 0x4B000000u;  // 2^23
-          const uint32_t lo = w[u], hi = w[u] >> 16;
-          x[c] = fmaf(__uint_as_float((lo & (15u << (4 * c))) | kBits) - 0x1p23f, s, b);
-          x[c + 4] = fmaf(__uint_as_float((hi & (15u << (4 * c))) | kBits) - 0x1p23f, s, b);
-          s *= 0.0625f;
-        }
+      for (int u = 0; u < 4 && u0 + u < kTasks; ++u) {
+        const int i = (u0 + u) * 4 + grp, rr = i >> 1;
         uint16_t* dst = (i & 1 ? p.v_out : p.k_out) + ((r0 + rr) * p.kv_heads + h) * D + lane * 8;
-        if (is[u])
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float b = sb_bias(sb[u][g]);
+          float x[8], s = sb_scale(sb[u][g]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // 16^c code times scale / 16^c: both exact, the sum is rounded once
+            constexpr uint32_t kBits = 0x4B000000u;  // 2^23
+            const uint32_t lo = w[u][g], hi = lo >> 16;
+            x[c] = fmaf(__uint_as_float((lo & (15u << (4 * c))) | kBits) - 0x1p23f, s, b);
+            x[c + 4] = fmaf(__uint_as_float((hi & (15u << (4 * c))) | kBits) - 0x1p23f, s, b);
+            s *= 0.0625f;
+          }
+          if (is[u])
+            *reinterpret_cast<uint4*>(dst + 64 * g) =
+                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        }
       }
     }
   }
