@@ -395,8 +395,10 @@ struct ApBlock {
     const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
     const uint32_t ts = tmem + lanes + Gm::kTmemS + 128 * x, to = tmem + lanes + Gm::kTmemO + D * x;
     const int tok = T.first + x * p.tile_tokens + row / p.group, head = kvh * p.group + row % p.group;
-    const bool live = row < p.tile_tokens * p.group && tok < T.nq;
-    const int sees = live ? tok + T.nk - T.nq + 1 : 0;
+    const bool whole = row < p.tile_tokens * p.group, live = whole && tok < T.nq;
+    // rows behind the tile's last token (where 128 is no multiple of G) have zeros for Q and go
+    // along, so that their warp leaves no keys out on their account
+    const int sees = live ? tok + T.nk - T.nq + 1 : whole ? 0 : T.nk;
     // (a scale of zero as one that changes no weight: a key left out stays at minus infinity)
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f), slack = kApSlack / c;
     float ref = -INFINITY, l = 0.f;
@@ -557,6 +559,10 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
     bar->abort_flag = 0;
     mbar_init_fence();
   }
+  // rows of the Q tiles that no load writes
+  for (int i = p.tile_tokens * p.group * 8 + threadIdx.x; i < kApRows * 8; i += Gm::kThreads)
+    for (int b = 0; b < X * Gm::kHalves; ++b) *reinterpret_cast<uint4*>(base + Gm::kQ + b * Gm::kBlock + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   grid_launch_dependents();
   grid_dependency_wait();
   ApBlock<D, X> B{p, base, bar};
