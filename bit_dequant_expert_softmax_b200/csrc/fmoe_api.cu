@@ -1090,3 +1090,5 @@ fmoe_status fmoe_layer_forward_noalloc(fmoe_layer_t L, const uint16_t* x, const 
 }
 
 }  // extern "C"
+
+#include "fmoe_attn_api.cuh"

@@ -1,4 +1,7 @@
-// C ABI of the attention layers (include/fmoe_attn.h): argument checks and launches.
+// C ABI of the attention layers (include/fmoe_attn.h): argument checks and launches.  Part of
+// fmoe_api.cu's translation unit.
+#pragma once
+
 #include <atomic>
 #include <cstdint>
 
@@ -18,8 +21,6 @@ constexpr int kMaxGridY = 65535;
 constexpr int kFewTokens = 480;  // fmoe_kv_append: 300 tokens of 32 + 2 x 4 heads take 6.3 us by blocks, 8.1 by warps; 600: 9.8, 8.5
 constexpr int kGatherWide = 400;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 5.9 us 64 rows a block, 5.0 us 16; 4000: 7.0, 8.0
 
-bool on_boundary(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 fmoe_status check_config(const fmoe_attn_config* c) {
   if (!c || c->kv_heads < 1 || c->kv_heads > kMaxGridY || c->q_heads < c->kv_heads || c->q_heads % c->kv_heads ||
       c->q_heads / c->kv_heads > 128 || c->head_dim < 1)
@@ -30,7 +31,7 @@ fmoe_status check_config(const fmoe_attn_config* c) {
 
 // Rows of `heads` heads, `stride` elements apart.
 bool rows_ok(const void* p, int64_t stride, int heads, int D) {
-  return p && on_boundary(p, 16) && stride >= (int64_t)heads * D && stride % 8 == 0;
+  return p && aligned(p, 16) && stride >= (int64_t)heads * D && stride % 8 == 0;
 }
 
 // Rows of bf16 in memory: `rows` of them, `stride` elements apart, `width` elements each.
@@ -121,22 +122,11 @@ fmoe_status gather(const KvGatherParams& p, int64_t rows, void* stream) {
                                               : launch(kv_gather_kernel<D, 16>, narrow, kKvThreads, 0, stream, p);
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // bf16 rows of `heads` heads as {D, heads, rows}, boxes of 64 channels x box_heads x box_rows
 // (128-byte swizzled rows of 64 channels in shared memory, rows outside as zeros).
 bool row_map(CUtensorMap* m, const uint16_t* base, int D, int heads, int64_t rows, int64_t stride, int box_heads,
              int box_rows) {
-  static const EncodeTiledFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
+  const EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
@@ -182,10 +172,10 @@ fmoe_status fmoe_kv_append(const fmoe_attn_config* c, const uint16_t* q, int64_t
   if (T == 0) return FMOE_OK;
   if ((q == nullptr) != (q_out == nullptr) || (q && !rows_ok(q, q_stride, c->q_heads, D))) return FMOE_ERR_INVALID_ARG;
   if (!rows_ok(k, k_stride, c->kv_heads, D) || !rows_ok(v, v_stride, c->kv_heads, D)) return FMOE_ERR_INVALID_ARG;
-  if (!slots || !on_boundary(slots, 8) || !cache || !on_boundary(cache, 128)) return FMOE_ERR_INVALID_ARG;
-  if (rotary && (!rope || !on_boundary(rope, 16) || !positions || !on_boundary(positions, 4) || rope_positions < 1))
+  if (!slots || !aligned(slots, 8) || !cache || !aligned(cache, 128)) return FMOE_ERR_INVALID_ARG;
+  if (rotary && (!rope || !aligned(rope, 16) || !positions || !aligned(positions, 4) || rope_positions < 1))
     return FMOE_ERR_INVALID_ARG;
-  if (!on_boundary(q_out, 16) || !on_boundary(k_out, 16) || !on_boundary(device_error, 4)) return FMOE_ERR_INVALID_ARG;
+  if (!aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(device_error, 4)) return FMOE_ERR_INVALID_ARG;
   const int64_t wide = (int64_t)c->q_heads * D, narrow = (int64_t)c->kv_heads * D;
   const Span sq{q, T, q_stride, wide}, sk{k, T, k_stride, narrow}, sv{v, T, v_stride, narrow};
   const Span oq{q_out, T, wide, wide}, ok{k_out, T, narrow, narrow};
@@ -224,9 +214,9 @@ fmoe_status fmoe_kv_gather(const fmoe_attn_config* c, const void* cache, int64_t
   if (st != FMOE_OK) return st;
   if (seqs < 0 || rows < 0 || rows > INT32_MAX || pages < 0 || table_width < 1) return FMOE_ERR_INVALID_ARG;
   if (seqs == 0 || rows == 0) return FMOE_OK;
-  if (!cache || !on_boundary(cache, 128) || !page_table || !on_boundary(page_table, 4) || !cu || !on_boundary(cu, 4) ||
-      !on_boundary(first, 4) || !k_out || !on_boundary(k_out, 16) || !v_out || !on_boundary(v_out, 16) ||
-      !on_boundary(device_error, 4))
+  if (!cache || !aligned(cache, 128) || !page_table || !aligned(page_table, 4) || !cu || !aligned(cu, 4) ||
+      !aligned(first, 4) || !k_out || !aligned(k_out, 16) || !v_out || !aligned(v_out, 16) ||
+      !aligned(device_error, 4))
     return FMOE_ERR_INVALID_ARG;
   const int64_t narrow = (int64_t)c->kv_heads * c->head_dim;
   if (meet(Span{k_out, rows, narrow, narrow}, Span{v_out, rows, narrow, narrow})) return FMOE_ERR_INVALID_ARG;
@@ -249,15 +239,15 @@ fmoe_status fmoe_attn_decode(const fmoe_attn_config* c, const uint16_t* q, int64
   if (seqs < 0 || pages < 0 || table_width < 1 || !(scale == scale) || (int64_t)table_width * c->page_tokens > (1 << 30))
     return FMOE_ERR_INVALID_ARG;
   if (seqs == 0) return FMOE_OK;
-  if (!rows_ok(q, q_stride, c->q_heads, D) || !cache || !on_boundary(cache, 128) || !page_table ||
-      !on_boundary(page_table, 4) || !lens || !on_boundary(lens, 4) || !out || !on_boundary(out, 16) ||
-      !on_boundary(device_error, 4))
+  if (!rows_ok(q, q_stride, c->q_heads, D) || !cache || !aligned(cache, 128) || !page_table ||
+      !aligned(page_table, 4) || !lens || !aligned(lens, 4) || !out || !aligned(out, 16) ||
+      !aligned(device_error, 4))
     return FMOE_ERR_INVALID_ARG;
   const int64_t row = (int64_t)c->q_heads * D;
   if (meet(Span{out, seqs, row, row}, Span{q, seqs, q_stride, row})) return FMOE_ERR_INVALID_ARG;
   const AdWorkspace w = decode_workspace(D);
   if (!workspace || workspace_bytes < w.size) return FMOE_ERR_NO_WORKSPACE;
-  if (!on_boundary(workspace, 256)) return FMOE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return FMOE_ERR_INVALID_ARG;
   int device = 0;
   const int sms = device_sms(&device);
   if (sms == 0) return FMOE_ERR_CUDA;
@@ -296,8 +286,8 @@ fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64
   if (seqs < 0 || q_rows < 0 || k_rows < 0 || q_rows > INT32_MAX || k_rows > INT32_MAX || !(scale == scale))
     return FMOE_ERR_INVALID_ARG;
   if (seqs == 0 || q_rows == 0) return FMOE_OK;
-  if (!rows_ok(q, q_stride, c->q_heads, D) || !cu_q || !on_boundary(cu_q, 4) || !cu_k || !on_boundary(cu_k, 4) || !out ||
-      !on_boundary(out, 16) || !on_boundary(device_error, 4))
+  if (!rows_ok(q, q_stride, c->q_heads, D) || !cu_q || !aligned(cu_q, 4) || !cu_k || !aligned(cu_k, 4) || !out ||
+      !aligned(out, 16) || !aligned(device_error, 4))
     return FMOE_ERR_INVALID_ARG;
   if (!rows_ok(k, k_stride, c->kv_heads, D) || !rows_ok(v, v_stride, c->kv_heads, D)) return FMOE_ERR_INVALID_ARG;
   const int64_t wide = (int64_t)c->q_heads * D, narrow = (int64_t)c->kv_heads * D;

@@ -136,7 +136,7 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t pari
 #ifndef FMOE_WAIT_SLEEP_NS
 #define FMOE_WAIT_SLEEP_NS 64
 #endif
-inline __device__ __noinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+__device__ __noinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                                uint32_t* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
@@ -192,10 +192,6 @@ __device__ __forceinline__ float chunk_unscale(int pre) {
 
 __device__ __forceinline__ void fma2(unsigned long long& acc, unsigned long long c, unsigned long long x) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(c), "l"(x));
-}
-
-__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
-  return (static_cast<unsigned long long>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
 }
 
 __device__ __forceinline__ float pair_sum(unsigned long long a) {
