@@ -101,8 +101,8 @@ def fmoe_attn_workspace_bytes(cfg: fmoe_attn_config) -> int:
 
 
 def attn_workspace(cfg: fmoe_attn_config, device="cuda"):
-    """A zeroed workspace for fmoe_attn_decode."""
-    return torch.zeros(fmoe_attn_workspace_bytes(cfg), dtype=torch.uint8, device=device)
+    """A workspace for fmoe_attn_decode."""
+    return torch.empty(fmoe_attn_workspace_bytes(cfg), dtype=torch.uint8, device=device)
 
 
 def kv_cache(cfg: fmoe_attn_config, pages: int, device="cuda"):

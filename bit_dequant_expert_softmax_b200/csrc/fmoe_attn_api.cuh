@@ -18,6 +18,7 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int kMaxGridY = 65535;
+constexpr float kScaleLimit = 0x1p24f;  // of a score's scale
 constexpr int kFewTokens = 480;  // fmoe_kv_append: 300 tokens of 32 + 2 x 4 heads take 6.3 us by blocks, 8.1 by warps; 600: 9.8, 8.5
 constexpr int kGatherWide = 400;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 5.9 us 64 rows a block, 5.0 us 16; 4000: 7.0, 8.0
 
@@ -236,7 +237,7 @@ fmoe_status fmoe_attn_decode(const fmoe_attn_config* c, const uint16_t* q, int64
   const fmoe_status st = check_config(c);
   if (st != FMOE_OK) return st;
   const int D = c->head_dim;
-  if (seqs < 0 || pages < 0 || table_width < 1 || !(scale == scale) || (int64_t)table_width * c->page_tokens > (1 << 30))
+  if (seqs < 0 || pages < 0 || table_width < 1 || !(scale > -kScaleLimit && scale < kScaleLimit) || (int64_t)table_width * c->page_tokens > (1 << 30))
     return FMOE_ERR_INVALID_ARG;
   if (seqs == 0) return FMOE_OK;
   if (!rows_ok(q, q_stride, c->q_heads, D) || !cache || !aligned(cache, 128) || !page_table ||
@@ -283,12 +284,13 @@ fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64
   const fmoe_status st = check_config(c);
   if (st != FMOE_OK) return st;
   const int D = c->head_dim;
-  if (seqs < 0 || q_rows < 0 || k_rows < 0 || q_rows > INT32_MAX || k_rows > INT32_MAX || !(scale == scale))
+  if (seqs < 0 || q_rows < 0 || k_rows < 0 || q_rows > INT32_MAX || k_rows > INT32_MAX || !(scale > -kScaleLimit && scale < kScaleLimit))
     return FMOE_ERR_INVALID_ARG;
   if (seqs == 0 || q_rows == 0) return FMOE_OK;
   if (!rows_ok(q, q_stride, c->q_heads, D) || !cu_q || !aligned(cu_q, 4) || !cu_k || !aligned(cu_k, 4) || !out ||
       !aligned(out, 16) || !aligned(device_error, 4))
     return FMOE_ERR_INVALID_ARG;
+  if (k_rows == 0) k = v = q, k_stride = v_stride = q_stride;  // no key: nothing of them is read
   if (!rows_ok(k, k_stride, c->kv_heads, D) || !rows_ok(v, v_stride, c->kv_heads, D)) return FMOE_ERR_INVALID_ARG;
   const int64_t wide = (int64_t)c->q_heads * D, narrow = (int64_t)c->kv_heads * D;
   const Span so{out, q_rows, wide, wide};

@@ -117,13 +117,13 @@ fmoe_status fmoe_kv_gather(const fmoe_attn_config* cfg, const void* cache, int64
  * A length beyond table_width * P is cut to it (and its bit set); the keys of a bad page
  * are left out (and its bit set).  A NaN or infinity in a cached key or value reaches the
  * outputs of its own sequence and key/value head only.
- * Range: |q| and the cached scales below 2^60 and |scale| below 2^48 (codes enter the products
- * as multiples of 2^-133 and the other operands carry 2^60 against them); queries below 2^-50
- * lose bits.
+ * Range: |scale| below 2^24 (else INVALID_ARG); |q| below 2^60, cached scales and biases below
+ * 2^30 (codes enter the products as multiples of 2^-133 and the other operands carry 2^60
+ * against them; beyond that the outputs of that sequence and head may overflow to infinities and
+ * NaN); queries below 2^-50 lose bits.
  *
- * workspace: fmoe_attn_workspace_bytes() bytes, 256-byte aligned, zeroed by the caller
- * before its first use; every call leaves it ready for the next, whatever its sizes and
- * config.  Calls (and replays of captured graphs) that share a workspace must not overlap.
+ * workspace: fmoe_attn_workspace_bytes() bytes, 256-byte aligned; what it holds before and
+ * after a call does not matter.  Calls (and replays of captured graphs) that share a workspace must not overlap.
  * seqs == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, NO_WORKSPACE, CUDA. */
 fmoe_status fmoe_attn_decode(const fmoe_attn_config* cfg, const uint16_t* q, int64_t q_stride, const void* cache,
                              int64_t pages, const int32_t* page_table, int table_width, const int32_t* lens, int seqs,
@@ -149,7 +149,8 @@ size_t fmoe_attn_workspace_bytes(const fmoe_attn_config* cfg);
  * decreasing ones, set FMOE_DEVERR_BAD_LENGTH and the sequences they bound are left out.
  * Rows of other sequences and rows behind the last one never reach a sequence's outputs,
  * whatever they hold; a NaN or infinity in a sequence's own q, k or v may reach any of its
- * outputs of that key/value head.  page_tokens is not used.
+ * outputs of that key/value head.  k and v may be NULL where k_rows is 0; |scale| is below 2^24
+ * (else INVALID_ARG); page_tokens is not used.
  * seqs == 0 or q_rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 fmoe_status fmoe_attn_prompt(const fmoe_attn_config* cfg, const uint16_t* q, int64_t q_stride, const uint16_t* k,
                              int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* cu_q,

@@ -125,6 +125,16 @@ def test_prompt_refusals(attn):
         assert _call(f, names, good, **bad) == 1, bad
 
 
+@pytest.mark.parametrize("scale", [2.0 ** 24, -2.0 ** 24, float("inf"), -float("inf")])
+def test_scales_out_of_range(attn, scale):
+    """Scores that would pass what fp32 holds."""
+    cfg = attn.fmoe_attn_config(4, 2, 64, 64)
+    size = attn.fmoe_attn_workspace_bytes(cfg)
+    assert attn.lib().fmoe_attn_decode(cfg.ref, A, 256, A, 2, A, 3, A, 2, scale, B, B, size, None, None) == 1
+    for k in (A, None):
+        assert attn.lib().fmoe_attn_prompt(cfg.ref, A, 256, k, 128, k, 128, A, A, 2, 10, 0, scale, B, None, None) == 1
+
+
 def test_binding_refuses_wrong_tensors(attn):
     """Tensors of a wrong type, shape or place are refused by the binding (status 1)."""
     import torch

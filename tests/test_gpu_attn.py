@@ -464,6 +464,17 @@ def test_prompt_bad_offsets(attn):
     _check_prompt(q, k, v, [0, 30], [0, 30], 0.1, out)
 
 
+def test_prompt_without_any_key(attn):
+    """Queries before the first key (no key rows at all): zeros, rows behind the last sequence left."""
+    rng = np.random.default_rng(12)
+    cfg = attn.fmoe_attn_config(6, 2, 128)
+    q, none = _bf16(rng, 140, 6, 128), torch.empty(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((140, 6, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = _err()
+    attn.fmoe_attn_prompt(cfg, q, none, none, _i32([0, 130, 139]), _i32([0, 0, 0]), out, 0.1, error=err)
+    assert int(err) == 0 and (out[:139] == 0).all() and (out[139] == 7).all()
+
+
 def test_prompt_large_scores(attn):
     rng = np.random.default_rng(11)
     cfg = attn.fmoe_attn_config(2, 1, 128)
