@@ -30,6 +30,13 @@
 // keeps its own sums; nothing waits for another warp until the block's end, where the parts of
 // pairs that lie in several of its warps are joined in shared memory.  A pair that lies in one
 // block goes to the output, parts of others to the workspace, where a second kernel joins them.
+// (Shares of 12 to 16 warps an SM instead of 8 to 12 with fewer registers, and shares weighted by a
+// block's start time, measured no better.)
+// Measured: 64 sequences of 200 to 16384 tokens, 32 over 8 heads of 128: 63.8 us (4.0 TB/s, 0.62 of the
+// measured copy bandwidth) with the issue slots at 52%, the integer and logic units at 49% and the tensor cores at
+// 26%: what bounds it is the unpacking between the loads' waits.  131072 tokens, 32 over 2 heads: 24.5 us, of
+// which the line's loop takes 11.5, start 6.6, the joins the rest.  One sequence of 777: 9.6 us, all of it
+// latency (launches 2.6 + 2, the plan 1.2, first data 1.7, arithmetic and merge 2).
 // Per query the exponentials refer to a value at most 2^8 below the running maximum, so that
 // the sums are rescaled a few times per pair and not at every new maximum.
 #pragma once
@@ -169,7 +176,6 @@ struct AdWarp {
   AdControl* all;              // of the block's warps
   AdControl* my;
   uint64_t* bars;
-  bool lost = false;           // a copy's wait ran out
   int page0 = 0, pages = 0;    // page table entries page0 .. of the pair being fetched, one per lane
 
   // online softmax state: columns 2t and 2t + 1 of every 8-query tile
@@ -265,16 +271,18 @@ struct AdWarp {
     return ok;
   }
 
-  __device__ __forceinline__ void wait(uint32_t slot, uint32_t parity) {
-    if (mbar_try_wait(&bars[slot], parity) || lost) return;
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(&bars[slot], parity)) {
-      if (global_timer_ns() - t0 > kAdWaitNs) {
-        lost = true;
-        kv_error(p.err, FMOE_DEVERR_COPY_TIMEOUT);
-        return;
+  // A bounded wait for the warp's copy number `copy`; false (for the whole warp) once the time is up.
+  __device__ __forceinline__ bool wait(uint32_t copy) {
+    uint64_t* bar = &bars[copy % Gm::kStages];
+    const uint32_t parity = (copy / Gm::kStages) & 1u;
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+      const uint64_t t0 = global_timer_ns();
+      while (!(ok = mbar_try_wait(bar, parity)) && global_timer_ns() - t0 <= kAdWaitNs) {
       }
+      if (!ok) kv_error(p.err, FMOE_DEVERR_COPY_TIMEOUT);
     }
+    return __all_sync(0xffffffffu, ok);
   }
 
   // query fragments and group sums of (sequence, head, query block); fresh softmax state
@@ -781,18 +789,20 @@ __global__ void __launch_bounds__(kAdThreads, AdGeom<D, NT>::kBlocks) attn_decod
     };
     refill();
     rest();  // while the first copies are on their way
+    bool ok = true;
     for (uint32_t at = 0; at < pushed; ++at) {
       const AdPart& r = W.my->part[at % kAdParts];
       W.start(r.seq, r.kvh, r.hb - r.kvh * p.qblocks);
       const int end = r.b, len = r.len;
       for (int lo = r.a; lo < end; lo += Gm::kTake) {
         const uint32_t slot = done % Gm::kStages;
-        W.wait(slot, (done / Gm::kStages) & 1u);
+        if (!(ok = W.wait(done))) break;
         W.step(slot, min(Gm::kTake, end - lo), (oks >> (4 * slot)) & 0xFu, lo * kKvTile, len);
         __syncwarp();
         ++done;
         refill();
       }
+      if (!ok) break;
       W.finish();
       if (r.a > 0) {
         W.put(W.head);
@@ -815,6 +825,8 @@ __global__ void __launch_bounds__(kAdThreads, AdGeom<D, NT>::kBlocks) attn_decod
         }
       }
     }
+    if (!ok)  // what is still in flight lands before the block ends
+      for (; done < issued; ++done) W.wait(done);
   }
   __syncthreads();
   // pairs that end in this warp and began before it
