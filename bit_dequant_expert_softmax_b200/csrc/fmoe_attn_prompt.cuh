@@ -6,22 +6,38 @@
 //   S = Q K^T  Q and K from shared memory (TMA, 128-byte swizzle), S in tensor memory
 //   O += P V   P (bf16) from tensor memory, written over S; V from shared memory with the keys
 //              along its rows as they come (the transposed-operand form)
-// A block holds two row tiles of 128, so that one tile's softmax runs while the tensor cores
-// work on the other's products.  A row is a (token, query head of the group) pair, G heads of one
-// token in adjacent rows: a tile has 128 / G tokens of all the heads that share a key/value
-// head, which reads K and V once for the group and keeps the causal waste at 128 / G tokens.
+// A row is a (token, query head of the group) pair, G heads of one token in adjacent rows: a
+// tile of 128 rows has 128 / G tokens of all the heads that share a key/value head, which reads K
+// and V once for the group and keeps the causal waste at 128 / G tokens.
 //
-//   warps 0-3, 4-7  softmax of row tile A, B: a thread owns a row (a tensor memory lane)
-//   warp 8          one lane issues every tcgen05.mma
-//   warp 9          one lane issues the TMA loads (warps 10, 11 fill up their warpgroup)
-// The launch gives every thread 168 registers; the softmax warps, which hold 128 scores each
-// thread, take 216 of them and the other warpgroup keeps 72 (216 * 256 + 72 * 128 = 168 * 384).
+// One tile's softmax runs while the tensor cores work on another's products.  The two tiles are
+// either one block's (X = 2), sharing the loads of K and V, or those of two blocks on an SM
+// (X = 1), where one block's beginning and end hide under the other's work too; the launch
+// chooses by the sequences' lengths and says what both take.
+//   warps 0-3 (4-7)  softmax of row tile 0 (1): a thread owns a row (a tensor memory lane)
+//   the next warp    issues every tcgen05.mma, converged with one elected lane: with a lone
+//                    lane in the code every product waited some 100 cycles for its operands' way
+//                    into uniform registers
+//   the next         one lane issues the TMA loads (at X = 2 two more fill up the warpgroup)
+// At X = 2 the launch gives every thread 168 registers; the softmax warps, which hold 128 scores
+// each thread, take 216 of them and the other warpgroup keeps 72 (216 * 256 + 72 * 128 = 168 * 384).
 //
 // The softmax keeps a reference r >= (running maximum - 8 in log2 units) per row: p = 2^(s - r)
 // is at most 2^8, and O, which lives in tensor memory, is rescaled only when a row's maximum
 // passes r by more than 8, which hardly ever happens after the first keys.  p is rounded to bf16
 // for the second product (V is bf16: the rounding weighs as much as V's own); its row sum is
 // taken in fp32 before the rounding.
+//
+// What bounds it: a step of 128 x 128 scores takes the tensor cores 1024 cycles (D = 128; 512 at
+// 64) and the exponential unit 1024 more, 16 a cycle, so that two tiles in turn can fill both.  2048
+// tokens of 32 over 8 heads of 128 take 40.9 us: exponential unit 47%, tensor cores 46% of the
+// time, the rest a block's start and end and the waits of one for the other.  8192 tokens
+// take 430 to 500 us (1.1 to 1.28 PFLOP/s of visible pairs) with the power limit holding the
+// clock at 1.5 to 1.65 GHz; 24 short prompts of 24 over 8 heads of 64 39 us, half of it
+// blocks' starts and ends.  Tried and slower there: part of the exponentials as polynomials on
+// the FMA units (which draw on the same power); score products of 64 keys in two buffers (twice
+// the instructions on operands half as wide); tensor memory allocated ahead of the wait for the
+// kernel before.
 //
 // V rows behind the sequence's last key belong to another sequence and may hold anything: they
 // are zeroed in shared memory (0 * NaN would pass through the product).
