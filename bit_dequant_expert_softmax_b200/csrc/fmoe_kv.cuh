@@ -250,6 +250,18 @@ __device__ __forceinline__ void load_nc(uint32_t (&w)[N], const uint8_t* src) {
   }
 }
 
+// bf16(scale code + bias) of codes 2c and 2c + 1 of a word.  A byte times 1 + 2^12 has its low nibble at
+// bit 0 and its high one at bit 16, where they become 128 + code by an OR, exactly; the product and
+// sum are rounded once, to bf16, which is what a rounding to fp32 in between would give: a product
+// (of 12 bits) whose low bits fp32 would drop is less than a sixteenth of a bf16 step of the bias.
+__device__ __forceinline__ uint32_t kv_value_pair(uint32_t w, int c, uint32_t sb) {
+  const uint32_t both = __byte_perm(w, 0u, 0x4440u + c) * 4097u;
+  uint32_t x = (both & 0x000F000Fu) | 0x43004300u, d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0x43004300u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(__byte_perm(sb, 0u, 0x1010u)), "r"(__byte_perm(sb, 0u, 0x3232u)));
+  return d;
+}
+
 struct KvGatherParams {
   const uint8_t* cache;
   long long pages, page_bytes, rows;
@@ -264,8 +276,7 @@ struct KvGatherParams {
 // finds its rows' sequences by counting those that end at or before each row, a lane then its
 // row's place in the cache (-1: none); eight lanes take one head's keys or values of one row, a
 // lane the same 8-channel block of every 64-channel group (one load of codes; the stores of a
-// group's blocks join to 128 bytes), several of them in flight.  Codes become floats in place,
-// as the low bits of 2^23.
+// group's blocks join to 128 bytes), several of them in flight.
 template <int D, int Rows>
 __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const __grid_constant__ KvGatherParams p) {
   using Gm = KvGeom<D>;
@@ -331,19 +342,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const __grid_cons
         uint16_t* dst = (i & 1 ? p.v_out : p.k_out) + ((r0 + rr) * p.kv_heads + h) * D + lane * 8;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float b = sb_bias(sb[u][g]);
-          float x[8], s = sb_scale(sb[u][g]);
+          uint32_t x[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {  // 16^c code times scale / 16^c: both exact, the sum is rounded once
-            constexpr uint32_t kBits = 0x4B000000u;  // 2^23
-            const uint32_t lo = w[u][g], hi = lo >> 16;
-            x[c] = fmaf(__uint_as_float((lo & (15u << (4 * c))) | kBits) - 0x1p23f, s, b);
-            x[c + 4] = fmaf(__uint_as_float((hi & (15u << (4 * c))) | kBits) - 0x1p23f, s, b);
-            s *= 0.0625f;
-          }
-          if (is[u])
-            *reinterpret_cast<uint4*>(dst + 64 * g) =
-                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+          for (int c = 0; c < 4; ++c) x[c] = kv_value_pair(w[u][g], c, sb[u][g]);
+          if (is[u]) *reinterpret_cast<uint4*>(dst + 64 * g) = make_uint4(x[0], x[1], x[2], x[3]);
         }
       }
     }
