@@ -19,8 +19,7 @@ namespace {
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int kMaxGridY = 65535;
 constexpr float kScaleLimit = 0x1p24f;  // of a score's scale
-constexpr int kFewTokens = 480;  // fmoe_kv_append: 300 tokens of 32 + 2 x 4 heads take 6.3 us by blocks, 8.1 by warps; 600: 9.8, 8.5
-constexpr int kGatherWide = 400;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 5.9 us 64 rows a block, 5.0 us 16; 4000: 7.0, 8.0
+constexpr int kGatherWide = 128;   // fmoe_kv_gather: 2000 rows of 8 heads of 128 take 4.2 us 64 rows a block, 4.8 us 16; 1000: 3.5 both; 1501 of 2 heads of 64: 3.2, 2.8
 
 fmoe_status check_config(const fmoe_attn_config* c) {
   if (!c || c->kv_heads < 1 || c->kv_heads > kMaxGridY || c->q_heads < c->kv_heads || c->q_heads % c->kv_heads ||
@@ -192,20 +191,19 @@ fmoe_status fmoe_kv_append(const fmoe_attn_config* c, const uint16_t* q, int64_t
   p.q_out = q_out, p.k_out = k_out, p.err = device_error;
   p.rope_positions = rope_positions, p.rotary = rotary;
   p.q_heads = c->q_heads, p.kv_heads = c->kv_heads, p.page_tokens = c->page_tokens;
-  // few tokens: one per block, their heads over several blocks, one per lane group;
-  // many: one per warp
-  const int per = kKvThreads / (D / 8), heads = (q ? c->q_heads : 0) + 2 * c->kv_heads;
-  p.tokens = T;
-  const bool few = T < kFewTokens;
-  const int groups = few ? per : 32 / (D / 8);
-  int y = few ? (heads + per - 1) / per : 1;
+  int device = 0;
+  const int sms = device_sms(&device);
+  if (sms == 0) return FMOE_ERR_CUDA;
+  const int per = kKvAppendThreads / (D / 8), heads = (q ? c->q_heads : 0) + 2 * c->kv_heads, most = (heads + per - 1) / per;
+  // blocks of a token: as many as the device has room for (300 tokens of 32 + 2 x 4 heads, with the gather
+  // behind: 7.1 us so, 8.3 with one block per 4 heads throughout; 1000: 10.2, 11.0 with one block)
+  int y = kKvAppendBlocks * sms / T;
+  y = y < 1 ? 1 : y > most ? most : y;
   if (y > kMaxGridY) y = kMaxGridY;
-  p.groups_log2 = __builtin_ctz(groups);
-  p.kv_turn = (groups * y - (q ? c->q_heads : 0) % (groups * y)) % (groups * y);
-  const int together = per / groups;
-  const dim3 grid((unsigned)((T + together - 1) / together), (unsigned)y);
-  return D == 128 ? launch(kv_append_kernel<128>, grid, kKvThreads, 0, stream, p)
-                  : launch(kv_append_kernel<64>, grid, kKvThreads, 0, stream, p);
+  p.kv_turn = (per * y - (q ? c->q_heads : 0) % (per * y)) % (per * y);
+  const dim3 grid((unsigned)T, (unsigned)y);
+  return D == 128 ? launch(kv_append_kernel<128>, grid, kKvAppendThreads, 0, stream, p)
+                  : launch(kv_append_kernel<64>, grid, kKvAppendThreads, 0, stream, p);
 }
 
 fmoe_status fmoe_kv_gather(const fmoe_attn_config* c, const void* cache, int64_t pages, const int32_t* page_table,

@@ -8,12 +8,12 @@
 // row, and thread g of eight the D/64 words of block g of a value row.
 //
 // Both move bytes: every row is read once, in 16-byte pieces per lane (append) or 4- and 8-byte ones
-// (gather), contiguous over the lanes of a head row, and written once.  Long calls run at 0.65
-// (append) and 0.78 (gather) of the measured copy bandwidth with the issue slots at 59% and about
+// (gather), contiguous over the lanes of a head row, and written once.  Long calls run at 0.73
+// (append) and 0.80 (gather) of the measured copy bandwidth with the issue slots at 59% and about
 // 70%, the quantiser's and the unpacking's instructions; short ones last as long as a launch and
 // three dependent loads (slot, row, rotation).
-// Measured: append, one token of 32 + 2 x 8 heads of 128 2.8 us, 8609 of 32 + 2 x 4 42 us (4.2
-// TB/s); gather, 1501 tokens of 2 heads of 64 2.8 us, 38059 of 8 heads of 128 39.6 us (5.05 TB/s).
+// Measured: append, one token of 32 + 2 x 8 heads of 128 2.8 us, 8609 of 32 + 2 x 4 37.6 us (4.7
+// TB/s); gather, 1501 tokens of 2 heads of 64 2.8 us, 38059 of 8 heads of 128 38.4 us (5.2 TB/s).
 // Eight lanes per row in the append as in the gather (16 channels a lane) gave nothing on long
 // calls and cost the short ones.
 #pragma once
@@ -29,6 +29,8 @@ namespace fmoe {
 
 constexpr int kKvTile = 16;      // tokens of a cache tile
 constexpr int kKvThreads = 256;
+constexpr int kKvAppendThreads = 64;
+constexpr int kKvAppendBlocks = 16;  // on an SM (64 registers a thread)
 constexpr int kKvAhead = 2;      // head rows of a lane group in flight
 
 template <int D>
@@ -74,7 +76,7 @@ struct KvAppendParams {
   long long pages, page_bytes;
   uint16_t *q_out, *k_out;
   uint32_t* err;
-  int tokens, groups_log2, kv_turn;  // kv_turn: key/value heads start where the query heads end
+  int kv_turn;  // kv_turn: key/value heads start where the query heads end
   int rope_positions, rotary, q_heads, kv_heads, page_tokens;
 };
 
@@ -121,25 +123,25 @@ __device__ __forceinline__ uint2 kv_quantise(const uint32_t (&w)[4], uint32_t ma
   return make_uint2(code, (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u));
 }
 
-// 2^groups_log2 of a block's lane groups take one token, whose heads they and blockIdx.y share out
-// (the query heads, then the key/value heads): all groups of a block and several blocks when
-// there are few tokens, one warp's when there are many, so that every warp has its own chain of
-// loads.  A lane owns 8 channels of a head row, which is one code word; a group's minimum and
-// maximum are reduced over its 8 lanes.  The token's cosines and sines of the lane's channels are
-// loaded once for all of its heads, and the first rows before the slot and position are looked at.
+// A block takes one token (blockIdx.x), whose heads the lane groups of all blocks with that token share
+// out (the query heads, then the key/value heads).  A lane owns 8 channels of a head row, which is one code
+// word; a group's minimum and maximum are reduced over its 8 lanes.  The token's cosines and sines
+// of the lane's channels are loaded once for all of its heads, and the first rows before the slot
+// and position are looked at.  Small blocks, because a token is short work and the last wave of
+// blocks waits for nobody else's (8609 tokens of 32 + 2 x 4 heads: 50 us with 8 tokens in a block of 256
+// threads and the gather behind it, 45 us so; 12 blocks of 85 registers on an SM 48.5).
 template <int D>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(kKvAppendThreads, kKvAppendBlocks) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   using Gm = KvGeom<D>;
-  constexpr int kPer = kKvThreads / Gm::kLanes;  // lane groups of a block
+  constexpr int kPer = kKvAppendThreads / Gm::kLanes;  // lane groups of a block
   grid_launch_dependents();
   grid_dependency_wait();
-  const int lane = threadIdx.x % Gm::kLanes, grp = threadIdx.x / Gm::kLanes, in = grp & ((1 << p.groups_log2) - 1);
+  const int lane = threadIdx.x % Gm::kLanes;
   const uint32_t mask = ((1u << Gm::kLanes) - 1) << (threadIdx.x & 31 & ~(Gm::kLanes - 1));  // the lane group
-  const long long tok = static_cast<long long>(blockIdx.x) * (kPer >> p.groups_log2) + (grp >> p.groups_log2);
-  if (tok >= p.tokens) return;
+  const long long tok = blockIdx.x;
   const int half = p.rotary / 2, c0 = lane * 8;
   const bool turned = c0 < p.rotary, first = c0 < half;
-  const int step = gridDim.y << p.groups_log2, id = (blockIdx.y << p.groups_log2) + in;
+  const int step = gridDim.y * kPer, id = blockIdx.y * kPer + threadIdx.x / Gm::kLanes;
   const int q_heads = p.q != nullptr ? p.q_heads : 0;
   const int pair = (first ? c0 + half : c0 - half) / 8;  // the lane with the other channels of the rotated pairs
   const uint16_t* q = p.q + tok * p.q_stride + c0;

@@ -100,6 +100,13 @@ def test_append_bytes(attn, H, KV, D, P, R, T, fused):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("H,KV,D,P,R,T,fused", [(18, 2, 128, 64, 64, 1100, False), (18, 2, 128, 16, 128, 2400, True),
+                                                (30, 1, 64, 32, 64, 1300, True)])
+def test_append_many_tokens(attn, H, KV, D, P, R, T, fused):
+    """So many that a token's heads lie in two blocks, or in one that goes round several times."""
+    test_append_bytes(attn, H, KV, D, P, R, T, fused)
+
+
 def test_append_in_place_without_queries_and_padding(attn):
     rng = np.random.default_rng(5)
     cfg = attn.fmoe_attn_config(4, 2, 128, 16)
