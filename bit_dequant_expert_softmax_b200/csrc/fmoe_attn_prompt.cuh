@@ -300,11 +300,9 @@ struct ApBlock {
     return true;
   }
 
-  // ---- loads: one lane
-  __device__ void load() {
+  // ---- loads: one lane.  The queries and the first keys go out before the block meets.
+  __device__ __forceinline__ void load_first() {
     const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * 128u;
-    int n = 0;
-    for (int x = 0; x < X; ++x) n = max(n, steps[x]);
     bool first = true;
     for (int x = 0; x < X; ++x) {
       if (steps[x] == 0) continue;
@@ -314,6 +312,10 @@ struct ApBlock {
       if (first) load_kv(0, true);
       first = false;
     }
+  }
+  __device__ void load() {
+    int n = 0;
+    for (int x = 0; x < X; ++x) n = max(n, steps[x]);
     int k = 1, v = 0;  // loads issued
     while (v < n && load_kv(v, false)) {
       if (++v == n || !load_kv(k, true)) break;
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
   uint8_t* base = ap_smem + ((1024u - (smem_u32(ap_smem) & 1023u)) & 1023u);
   ApBars* bar = reinterpret_cast<ApBars*>(base + Gm::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32 * Gm::kLoadWarp) {
     for (int i = 0; i < X; ++i) {
       mbar_init(&bar->q_full[i], 1);
       mbar_init(&bar->s_full[i], 1);
@@ -593,6 +595,7 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
     B.short_[x] = keys > 0 && (keys - 1) % kApKeys < kApKeys / 2;
     some |= keys > 0;
   }
+  if (some && threadIdx.x == 32 * Gm::kLoadWarp) B.load_first();
   if (warp == Gm::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar->tmem)), "r"(Gm::kTmem)
                  : "memory");
