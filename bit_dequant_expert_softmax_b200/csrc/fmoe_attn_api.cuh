@@ -137,16 +137,21 @@ bool row_map(CUtensorMap* m, const uint16_t* base, int D, int heads, int64_t row
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int X>
-fmoe_status prompt(ApParams& p, int64_t q_rows, int device, void* stream) {
+template <int D, int X, bool Waves>
+fmoe_status prompt_launch(const ApParams& p, int64_t blocks, int device, void* stream) {
   static std::atomic<uint64_t> done{0};
   using Gm = ApGeom<D, X>;
+  if (!opt_in(attn_prompt_kernel<D, X, Waves>, Gm::kSmem, device, done)) return FMOE_ERR_CUDA;
+  return launch(attn_prompt_kernel<D, X, Waves>, dim3((unsigned)blocks), Gm::kThreads, Gm::kSmem, stream, p);
+}
+// More blocks than the device holds at once take over one another's work.
+template <int D, int X>
+fmoe_status prompt(const ApParams& p, int64_t q_rows, int sms, int device, void* stream) {
   // units of X tiles of queries: at most this many over all sequences
-  const int64_t units = q_rows / (X * p.tile_tokens) + p.seqs;
-  if (units * p.kv_heads > INT32_MAX) return FMOE_ERR_UNSUPPORTED;
-  p.units = (int)units;
-  if (!opt_in(attn_prompt_kernel<D, X>, Gm::kSmem, device, done)) return FMOE_ERR_CUDA;
-  return launch(attn_prompt_kernel<D, X>, dim3((unsigned)(units * p.kv_heads)), Gm::kThreads, Gm::kSmem, stream, p);
+  const int64_t blocks = (q_rows / (X * p.tile_tokens) + p.seqs) * p.kv_heads;
+  if (blocks > INT32_MAX) return FMOE_ERR_UNSUPPORTED;
+  return blocks > sms * ApGeom<D, X>::kBlocks ? prompt_launch<D, X, true>(p, blocks, device, stream)
+                                              : prompt_launch<D, X, false>(p, blocks, device, stream);
 }
 
 }  // namespace
@@ -314,8 +319,8 @@ fmoe_status fmoe_attn_prompt(const fmoe_attn_config* c, const uint16_t* q, int64
   // Two against one, 32 over 8 heads of 128: 2048 tokens 40 and 45 us, 2 x 1024 28 and 32;
   // 1024 (128 blocks of two) 20.4 and 19.2, 16 x 512 76.4 and 73.7, 333 11.6 and 11.0.
   const bool pairs = k_rows / seqs >= 640 && q_rows / (2 * p.tile_tokens) * c->kv_heads >= sms;
-  if (D == 128) return pairs ? prompt<128, 2>(p, q_rows, device, stream) : prompt<128, 1>(p, q_rows, device, stream);
-  return pairs ? prompt<64, 2>(p, q_rows, device, stream) : prompt<64, 1>(p, q_rows, device, stream);
+  if (D == 128) return pairs ? prompt<128, 2>(p, q_rows, sms, device, stream) : prompt<128, 1>(p, q_rows, sms, device, stream);
+  return pairs ? prompt<64, 2>(p, q_rows, sms, device, stream) : prompt<64, 1>(p, q_rows, sms, device, stream);
 }
 
 }  // extern "C"

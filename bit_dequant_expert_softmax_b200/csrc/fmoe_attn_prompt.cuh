@@ -12,13 +12,14 @@
 //
 // One tile's softmax runs while the tensor cores work on another's products.  The two tiles are
 // either one block's (X = 2), sharing the loads of K and V, or those of two blocks on an SM
-// (X = 1), where one block's beginning and end hide under the other's work too; the launch
-// chooses by the sequences' lengths and says what both take.
+// (X = 1), which leaves no tile without a partner at a sequence's end; the launch chooses by the
+// sequences' lengths and says what both take.
 //   warps 0-3 (4-7)  softmax of row tile 0 (1): a thread owns a row (a tensor memory lane)
 //   the next warp    issues every tcgen05.mma, converged with one elected lane: with a lone
 //                    lane in the code every product waited some 100 cycles for its operands' way
 //                    into uniform registers
-//   the next         one lane issues the TMA loads (at X = 2 two more fill up the warpgroup)
+//   the next         finds the block's units, one lane issues the TMA loads (at X = 2 two more warps fill
+//                    up the warpgroup)
 // At X = 2 the launch gives every thread 168 registers; the softmax warps, which hold 128 scores
 // each thread, take 216 of them and the other warpgroup keeps 72 (216 * 256 + 72 * 128 = 168 * 384).
 //
@@ -30,11 +31,11 @@
 //
 // What bounds it: a step of 128 x 128 scores takes the tensor cores 1024 cycles (D = 128; 512 at
 // 64) and the exponential unit 1024 more, 16 a cycle, so that two tiles in turn can fill both.  2048
-// tokens of 32 over 8 heads of 128 take 40.9 us: exponential unit 47%, tensor cores 46% of the
+// tokens of 32 over 8 heads of 128 take 39.2 us: exponential unit 47%, tensor cores 46% of the
 // time, the rest a block's start and end and the waits of one for the other.  8192 tokens
 // take 430 to 500 us (1.1 to 1.28 PFLOP/s of visible pairs) with the power limit holding the
-// clock at 1.5 to 1.65 GHz; 24 short prompts of 24 over 8 heads of 64 39 us, half of it
-// blocks' starts and ends.  Tried and slower there: part of the exponentials as polynomials on
+// clock at 1.5 to 1.65 GHz; 24 short prompts of 24 over 8 heads of 64 36.8 us, of 2 to 7
+// dependent steps each.  Tried and slower there: part of the exponentials as polynomials on
 // the FMA units (which draw on the same power); score products of 64 keys in two buffers (twice
 // the instructions on operands half as wide); tensor memory allocated ahead of the wait for the
 // kernel before.
@@ -60,7 +61,7 @@ struct alignas(64) ApParams {
   uint16_t* out;
   uint32_t* err;
   float scale_log2;  // scale * log2(e)
-  int seqs, q_heads, kv_heads, group, tile_tokens, units;
+  int seqs, q_heads, kv_heads, group, tile_tokens;
 };
 
 // X row tiles per block
@@ -84,22 +85,32 @@ struct ApGeom {
   static constexpr uint32_t kTmemS = 0, kTmemO = 128 * X, kTmem = 256 * X;  // columns: S of tile x at 128 x, O behind them at D x
 };
 
+// The sequence and first query of a unit of the packed sequences' line of row tiles.
+struct ApTile {
+  int q0, nq, k0, nk;  // the sequence's rows
+  int first;           // the unit's first query in it
+};
+struct alignas(16) ApWork {
+  ApTile T;
+  int kvh;
+  int steps[2], short_[2];  // as ApBlock's
+  int go;                   // 0 behind the block's last unit
+};
+
 struct ApBars {
-  uint64_t q_full[2];
+  alignas(16) uint4 answer;                  // to the request for another block's work
+  uint64_t answered;
+  uint64_t work_full[2], work_empty[2];
+  uint64_t q_full[2], q_free[2];             // q_free: the unit's output has left the tile's Q rows
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: the first and the second half of the keys
   uint64_t drain;
   int abort_flag;
   uint32_t tmem;
+  ApWork work[2];
 };
 static_assert(sizeof(ApBars) <= 512, "barrier block");
 
-// The sequence and first query of row block `tile` of the packed sequences' line of blocks;
-// false behind the last one.  Every warp finds it for itself.
-struct ApTile {
-  int q0, nq, k0, nk;  // the sequence's rows
-  int first;           // the block's first query in it
-};
 __device__ __forceinline__ bool ap_span(const int32_t* cu, int s, long long rows, int& lo, int& n) {
   lo = __ldg(cu + s);
   const int hi = __ldg(cu + s + 1);
@@ -110,38 +121,87 @@ __device__ __forceinline__ bool ap_span(const int32_t* cu, int s, long long rows
   }
   return true;
 }
-__device__ __forceinline__ bool ap_find(const ApParams& p, long long tile, int tile_tokens, ApTile& r) {
-  const int lane = threadIdx.x & 31;
-  long long base = 0;
-  for (int s0 = 0; s0 < p.seqs; s0 += 32) {
-    int q0 = 0, nq = 0, k0 = 0, nk = 0;
-    if (s0 + lane < p.seqs) {
-      const bool a = ap_span(p.cu_q, s0 + lane, p.q_rows, q0, nq), b = ap_span(p.cu_k, s0 + lane, p.k_rows, k0, nk);
-      if (!a || !b) {
-        nq = 0;
-        kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
-      }
+// This lane's sequence of a round of 32, and its tiles; what is out of range has none.
+__device__ __forceinline__ int ap_round(const ApParams& p, int s, int tile_tokens, ApTile& r) {
+  r.q0 = r.nq = r.k0 = r.nk = 0;
+  if (s < p.seqs) {
+    const bool a = ap_span(p.cu_q, s, p.q_rows, r.q0, r.nq), b = ap_span(p.cu_k, s, p.k_rows, r.k0, r.nk);
+    if (!a || !b) {
+      r.nq = 0;
+      kv_error(p.err, FMOE_DEVERR_BAD_LENGTH);
     }
-    const int mine = (nq + tile_tokens - 1) / tile_tokens;
-    long long upto = mine;
+  }
+  return (r.nq + tile_tokens - 1) / tile_tokens;
+}
+// A warp's view of the line of units: a lane holds a sequence of one round of 32, and how many
+// units there are up to its end.  The round stays for the next search.
+struct ApLine {
+  ApTile own;
+  int mine, s0;
+  long long base, upto, total;
+
+  __device__ __forceinline__ void round(const ApParams& p, int from, long long before, int tile_tokens) {
+    const int lane = threadIdx.x & 31;
+    s0 = from;
+    base = before;
+    mine = ap_round(p, s0 + lane, tile_tokens, own);
+    upto = mine;
 #pragma unroll
     for (int x = 1; x < 32; x *= 2) {
       const long long y = __shfl_up_sync(0xffffffffu, upto, x);
       if (lane >= x) upto += y;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, base + upto > tile);
-    if (past != 0) {
-      const int who = __ffs(past) - 1;
-      r.q0 = __shfl_sync(0xffffffffu, q0, who);
-      r.nq = __shfl_sync(0xffffffffu, nq, who);
-      r.k0 = __shfl_sync(0xffffffffu, k0, who);
-      r.nk = __shfl_sync(0xffffffffu, nk, who);
-      r.first = static_cast<int>(tile - (base + __shfl_sync(0xffffffffu, upto - mine, who))) * tile_tokens;
-      return true;
-    }
-    base += __shfl_sync(0xffffffffu, upto, 31);
+    upto += base;
   }
-  return false;
+  // the rounds in turn from `from` on until one ends behind `at`
+  __device__ __forceinline__ void seek(const ApParams& p, int from, long long before, long long at, int tile_tokens) {
+    do {
+      round(p, from, before, tile_tokens);
+      before = __shfl_sync(0xffffffffu, upto, 31);
+      from += 32;
+    } while (from < p.seqs && before <= at);
+  }
+  __device__ __forceinline__ void begin(const ApParams& p, int tile_tokens) {
+    seek(p, 0, 0, INT64_MAX, tile_tokens);
+    total = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  // the unit at place `at` < total
+  __device__ __forceinline__ void find(const ApParams& p, long long at, int tile_tokens, ApTile& r) {
+    if (at < base || at >= __shfl_sync(0xffffffffu, upto, 31)) {
+      if (at < base)
+        seek(p, 0, 0, at, tile_tokens);
+      else
+        seek(p, s0 + 32, __shfl_sync(0xffffffffu, upto, 31), at, tile_tokens);
+    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+    r.q0 = __shfl_sync(0xffffffffu, own.q0, who);
+    r.nq = __shfl_sync(0xffffffffu, own.nq, who);
+    r.k0 = __shfl_sync(0xffffffffu, own.k0, who);
+    r.nk = __shfl_sync(0xffffffffu, own.nk, who);
+    r.first = static_cast<int>(at - __shfl_sync(0xffffffffu, upto - mine, who)) * tile_tokens;
+  }
+};
+
+// Asks for the work of a block that has not started: 16 bytes to `answer`, counted by `bar`.
+__device__ __forceinline__ void ap_ask(uint4* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// That block's index, which does not start any more; false: all have.
+__device__ __forceinline__ bool ap_answer(const uint4* answer, uint32_t& block) {
+  uint32_t is, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\tld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+      : "=&r"(is), "=&r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  block = x;
+  return is != 0;
 }
 
 // Shared-memory descriptors of 128-byte swizzled operands (1024-byte aligned blocks of 128-byte
@@ -269,7 +329,8 @@ __device__ __forceinline__ unsigned long long fadd2(unsigned long long a, unsign
   return d;
 }
 
-template <int D, int X>
+// Waves: more blocks than the device holds at once, and a block takes over others' work
+template <int D, int X, bool Waves>
 struct ApBlock {
   using Gm = ApGeom<D, X>;
   const ApParams& p;
@@ -279,6 +340,37 @@ struct ApBlock {
   int kvh;
   int steps[X];    // key steps of the row tiles
   bool short_[X];  // the last of them sees no key of its second half
+
+  int n;           // the longest of them
+
+  __device__ __forceinline__ void plan() {
+    n = 0;
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      const int t0 = T.first + x * p.tile_tokens, last = min(T.nq, t0 + p.tile_tokens) - 1;
+      const int keys = t0 < T.nq ? max(0, last + T.nk - T.nq + 1) : 0;
+      steps[x] = (keys + kApKeys - 1) / kApKeys;
+      short_[x] = keys > 0 && (keys - 1) % kApKeys < kApKeys / 2;
+      n = max(n, steps[x]);
+    }
+  }
+  // The block's unit number t, from the queue (a whole warp); false behind the last.
+  __device__ __forceinline__ bool next(int t) {
+    if (!__all_sync(0xffffffffu, wait(&bar->work_full[t & 1], (t >> 1) & 1))) return false;
+    const ApWork w = bar->work[t & 1];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar->work_empty[t & 1]);
+    T = w.T;
+    kvh = w.kvh;
+    n = 0;
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      steps[x] = w.steps[x];
+      short_[x] = w.short_[x] != 0;
+      n = max(n, steps[x]);
+    }
+    return w.go != 0;
+  }
 
   __device__ __forceinline__ uint8_t* q_at(int x) const { return base + Gm::kQ + x * Gm::kHalves * Gm::kBlock; }
   __device__ __forceinline__ uint8_t* k_at(int s) const { return base + Gm::kK + s * Gm::kHalves * Gm::kBlock; }
@@ -300,51 +392,114 @@ struct ApBlock {
     return true;
   }
 
-  // ---- loads: one lane.  The queries and the first keys go out before the block meets.
-  __device__ __forceinline__ void load_first() {
+  // ---- units and loads: a warp, its first lane issuing.  The next unit is asked for once the last
+  // scores of this one are there: early enough that its first loads go out under the rest of
+  // this one's work, and no earlier, so that a block with much left takes nothing from the others.
+  ApLine line;
+  uint32_t k_use, v_use, q_use[X];  // loads issued
+  bool has;                         // a unit at hand
+  // unit `back` from the line's end, of head kvh
+  __device__ __forceinline__ void find(int back) {
+    const long long at = line.total - 1 - back;
+    has = at >= 0;
+    if (!has) return;
+    line.find(p, at, X * p.tile_tokens, T);
+    plan();
+  }
+  // before the block meets: the first unit and its first loads
+  __device__ __forceinline__ void begin() {
+    k_use = v_use = 0;
+#pragma unroll
+    for (int x = 0; x < X; ++x) q_use[x] = 0;
+    // heads fastest and a sequence's last queries, which see the most keys, first
+    const int back = blockIdx.x / p.kv_heads;
+    kvh = blockIdx.x % p.kv_heads;
+    line.begin(p, X * p.tile_tokens);
+    find(back);
+    if (has && (threadIdx.x & 31) == 0) load_head(0);
+  }
+  __device__ void load() {
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+    int t = 0;
+    for (uint32_t asks = 0;; ++asks) {
+      if (lane == 0) {
+        if (has) ok = load_rest();
+        if (ok && Waves) ap_ask(&bar->answer, &bar->answered);
+      }
+      t += has;
+      if (!(ok = all(ok)) || !Waves) break;
+      if (!(ok = all(wait(&bar->answered, asks & 1, true)))) break;
+      uint32_t block;
+      const bool more = ap_answer(&bar->answer, block);
+      fence_proxy_async_smem();  // read before the next answer is written
+      __syncwarp();
+      if (!more) break;
+      kvh = block % p.kv_heads;
+      find(block / p.kv_heads);
+      if (!has) continue;
+      if (lane == 0) ok = load_head(t);
+      if (!(ok = all(ok))) break;
+    }
+    if (lane != 0) return;
+    if (ok && (t == 0 || Waves) && room(t)) {
+      bar->work[t & 1].go = 0;
+      mbar_arrive(&bar->work_full[t & 1]);
+    }
+    // copies still in flight land before the block ends
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+      if (q_use[x] > 0) wait(&bar->q_full[x], (q_use[x] - 1) & 1, true);
+    constexpr uint32_t S = Gm::kStages;
+    for (uint32_t i = k_use > S ? k_use - S : 0; i < k_use; ++i) wait(&bar->k_full[i % S], (i / S) & 1, true);
+    for (uint32_t i = v_use > S ? v_use - S : 0; i < v_use; ++i) wait(&bar->v_full[i % S], (i / S) & 1, true);
+  }
+  __device__ __forceinline__ bool room(int t) const { return t < 2 || wait(&bar->work_empty[t & 1], ((t >> 1) - 1) & 1); }
+  // unit t to the others, its first keys and its queries
+  __device__ __forceinline__ bool load_head(int t) {
+    if (!room(t)) return false;
+    bar->work[t & 1] = ApWork{T, kvh, {steps[0], steps[X - 1]}, {short_[0], short_[X - 1]}, 1};
+    mbar_arrive(&bar->work_full[t & 1]);
     const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * 128u;
-    bool first = true;
+    if (n > 0 && !load_kv(0, true)) return false;
+#pragma unroll
     for (int x = 0; x < X; ++x) {
+      if (t > 0 && !wait(&bar->q_free[x], (t - 1) & 1)) return false;
       if (steps[x] == 0) continue;
       mbar_arrive_expect_tx(&bar->q_full[x], q_bytes * Gm::kHalves);
       for (int h = 0; h < Gm::kHalves; ++h)
         tma_load_3d(q_at(x) + h * Gm::kBlock, &p.tm_q, &bar->q_full[x], 64 * h, kvh * p.group, T.q0 + T.first + x * p.tile_tokens);
-      if (first) load_kv(0, true);
-      first = false;
+      ++q_use[x];
     }
+    return true;
   }
-  __device__ void load() {
-    int n = 0;
-    for (int x = 0; x < X; ++x) n = max(n, steps[x]);
-    int k = 1, v = 0;  // loads issued
-    while (v < n && load_kv(v, false)) {
-      if (++v == n || !load_kv(k, true)) break;
-      ++k;
-    }
-    // copies still in flight land before the block ends
-    for (int x = 0; x < X; ++x)
-      if (steps[x] > 0) wait(&bar->q_full[x], 0, true);
-    for (int i = max(0, k - Gm::kStages); i < k; ++i) wait(&bar->k_full[i % Gm::kStages], (i / Gm::kStages) & 1, true);
-    for (int i = max(0, v - Gm::kStages); i < v; ++i) wait(&bar->v_full[i % Gm::kStages], (i / Gm::kStages) & 1, true);
+  // the rest of its loads, and its last scores
+  __device__ __forceinline__ bool load_rest() {
+    for (int j = 0; j < n; ++j)
+      if (!load_kv(j, false) || (j + 1 < n && !load_kv(j + 1, true))) return false;
+    const uint32_t last = k_use - 1;
+    return n == 0 || wait(&bar->k_empty[last % Gm::kStages], (last / Gm::kStages) & 1);
   }
   __device__ __forceinline__ bool load_kv(int j, bool key) {
-    const int s = j % Gm::kStages, use = j / Gm::kStages;
+    const uint32_t u = key ? k_use : v_use, s = u % Gm::kStages, use = u / Gm::kStages;
     uint64_t* full = key ? &bar->k_full[s] : &bar->v_full[s];
     if (use > 0 && !wait(key ? &bar->k_empty[s] : &bar->v_empty[s], (use - 1) & 1)) return false;
     mbar_arrive_expect_tx(full, Gm::kHalves * Gm::kBlock);
     for (int h = 0; h < Gm::kHalves; ++h)
       tma_load_3d((key ? k_at(s) : v_at(s)) + h * Gm::kBlock, key ? &p.tm_k : &p.tm_v, full, 64 * h, kvh, T.k0 + j * kApKeys);
+    (key ? k_use : v_use) = u + 1;
     return true;
   }
 
   // ---- products: the whole warp, one lane issuing.  Products of one thread run in the order of
   // their issue, so S(j + 1) may be issued behind the product that reads P(j) from the same columns.
   __device__ __forceinline__ bool all(bool ok) const { return __all_sync(0xffffffffu, ok); }
-  __device__ __forceinline__ bool keys(int j) const { return all(wait(&bar->k_full[j % Gm::kStages], (j / Gm::kStages) & 1)); }
-  __device__ __forceinline__ void score(uint32_t leads, int x, int j, uint32_t tmem, uint32_t smem) {
+  __device__ __forceinline__ bool keys(uint32_t j) const {  // (loads of K and of V count through the block's units)
+    return all(wait(&bar->k_full[j % Gm::kStages], (j / Gm::kStages) & 1)); }
+  __device__ __forceinline__ void score(uint32_t leads, int x, uint32_t use, uint32_t tmem, uint32_t smem) {
     const uint32_t idesc = ap_idesc(kApKeys, p.scale_log2 < 0.f, false);  // the softmax goes by |scale|
     const uint64_t a = ap_desc(smem + Gm::kQ + x * Gm::kHalves * Gm::kBlock, 16);
-    const uint64_t b = ap_desc(smem + Gm::kK + j % Gm::kStages * Gm::kHalves * Gm::kBlock, 16);
+    const uint64_t b = ap_desc(smem + Gm::kK + use % Gm::kStages * Gm::kHalves * Gm::kBlock, 16);
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       const uint64_t at = (static_cast<uint64_t>(c / 4) * Gm::kBlock + (c % 4) * 32) >> 4;
@@ -352,56 +507,64 @@ struct ApBlock {
     }
     ap_commit(leads, &bar->s_full[x]);
   }
-  // half h of the keys, the first and / or the last that the step multiplies
-  __device__ __forceinline__ void value(uint32_t leads, int x, int j, int h, bool first, bool last, uint32_t tmem, uint32_t smem) {
+  // half h of the keys, the first and / or the last that the step multiplies; `fresh`: the unit's first step
+  __device__ __forceinline__ void value(uint32_t leads, int x, uint32_t use, int h, bool fresh, bool first, bool last, uint32_t tmem,
+                                        uint32_t smem) {
     const uint32_t idesc = ap_idesc(D, false, true);
-    const uint64_t b = ap_desc(smem + Gm::kV + j % Gm::kStages * Gm::kHalves * Gm::kBlock, Gm::kBlock);
+    const uint64_t b = ap_desc(smem + Gm::kV + use % Gm::kStages * Gm::kHalves * Gm::kBlock, Gm::kBlock);
 #pragma unroll
     for (int c = 4 * h; c < 4 * h + 4; ++c)
       ap_mma_ts(leads, tmem + Gm::kTmemO + D * x, tmem + Gm::kTmemS + 128 * x + Gm::kP * h + 8 * (c % 4), b + ((c * 2048) >> 4), idesc,
-                j > 0 || !first || c % 4 > 0);
+                !fresh || !first || c % 4 > 0);
     if (last) ap_commit(leads, &bar->o_full[x]);
   }
   __device__ void multiply(uint32_t tmem_any) {
     const uint32_t leads = elect_lane();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0), smem = __shfl_sync(0xffffffffu, smem_u32(base), 0);
-    int nx[X], n = 0;
-    bool cut[X];
+    uint32_t use = 0, q_seen[X], p_seen[X][2];  // loads, and phases of q_full and p_full, so far
 #pragma unroll
-    for (int x = 0; x < X; ++x) {
-      nx[x] = __shfl_sync(0xffffffffu, steps[x], 0);
-      cut[x] = __any_sync(0xffffffffu, short_[x]);
-      n = max(n, nx[x]);
-    }
-    bool ok = keys(0);
-#pragma unroll
-    for (int x = 0; x < X; ++x) {
-      if (!ok || nx[x] == 0) continue;
-      ok = all(wait(&bar->q_full[x], 0));
-      tc_fence_after();
-      if (ok) score(leads, x, 0, tmem, smem);
-    }
-    ap_commit(leads, &bar->k_empty[0]);
-    for (int j = 0; j < n && ok; ++j) {
-      const bool more = j + 1 < n;
-      ok = all(wait(&bar->v_full[j % Gm::kStages], (j / Gm::kStages) & 1)) && (!more || keys(j + 1));
+    for (int x = 0; x < X; ++x) q_seen[x] = p_seen[x][0] = p_seen[x][1] = 0;
+    bool ok = true;
+    for (int t = 0; ok && (t == 0 || Waves) && next(t); ++t) {
+      int nx[X];
+      bool cut[X];
 #pragma unroll
       for (int x = 0; x < X; ++x) {
-        if (!ok || j >= nx[x]) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int h = Gm::kTwice ? 1 - i : i;
-          const bool one = cut[x] && j + 1 == nx[x];
-          if (!ok || (one && h == 1)) continue;
-          if (!(ok = all(wait(&bar->p_full[x][h], j & 1)))) continue;
-          tc_fence_after();
-          value(leads, x, j, h, one || i == 0, one || i == 1, tmem, smem);
-        }
-        if (ok && j + 1 < nx[x]) score(leads, x, j + 1, tmem, smem);
+        nx[x] = __shfl_sync(0xffffffffu, steps[x], 0);
+        cut[x] = __any_sync(0xffffffffu, short_[x]);
       }
-      if (!ok) break;
-      ap_commit(leads, &bar->v_empty[j % Gm::kStages]);
-      if (more) ap_commit(leads, &bar->k_empty[(j + 1) % Gm::kStages]);
+      const int most = __shfl_sync(0xffffffffu, n, 0);
+      if (most == 0) continue;
+      ok = keys(use);
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        if (!ok || nx[x] == 0) continue;
+        ok = all(wait(&bar->q_full[x], q_seen[x]++ & 1));
+        tc_fence_after();
+        if (ok) score(leads, x, use, tmem, smem);
+      }
+      ap_commit(leads, &bar->k_empty[use % Gm::kStages]);
+      for (int j = 0; j < most && ok; ++j, ++use) {
+        const bool more = j + 1 < most;
+        ok = all(wait(&bar->v_full[use % Gm::kStages], (use / Gm::kStages) & 1)) && (!more || keys(use + 1));
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+          if (!ok || j >= nx[x]) continue;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int h = Gm::kTwice ? 1 - i : i;
+            const bool one = cut[x] && j + 1 == nx[x];
+            if (!ok || (one && h == 1)) continue;
+            if (!(ok = all(wait(&bar->p_full[x][h], p_seen[x][h]++ & 1)))) continue;
+            tc_fence_after();
+            value(leads, x, use, h, j == 0, one || i == 0, one || i == 1, tmem, smem);
+          }
+          if (ok && j + 1 < nx[x]) score(leads, x, use + 1, tmem, smem);
+        }
+        if (!ok) break;
+        ap_commit(leads, &bar->v_empty[use % Gm::kStages]);
+        if (more) ap_commit(leads, &bar->k_empty[(use + 1) % Gm::kStages]);
+      }
     }
     ap_commit(leads, &bar->drain);  // nothing reads or writes tensor memory after this
     wait(&bar->drain, 0, true);
@@ -409,6 +572,15 @@ struct ApBlock {
 
   // ---- softmax of row tile x: thread = row
   __device__ void soften(int x, uint32_t tmem) {
+    uint32_t done = 0, use = 0;  // steps of the tile, loads of V, so far
+    for (int t = 0; (t == 0 || Waves) && next(t); ++t) {
+      const int mine = x == 0 ? steps[0] : steps[X - 1];
+      if (!soften(x, mine, x == 0 ? short_[0] : short_[X - 1], tmem, done, use)) return;
+      done += mine;
+      use += n;
+    }
+  }
+  __device__ __forceinline__ bool soften(int x, int mine, bool cut, uint32_t tmem, uint32_t done, uint32_t use) {
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
     const uint32_t ts = tmem + lanes + Gm::kTmemS + 128 * x, to = tmem + lanes + Gm::kTmemO + D * x;
@@ -420,8 +592,8 @@ struct ApBlock {
     // (a scale of zero as one that changes no weight: a key left out stays at minus infinity)
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f), slack = kApSlack / c;
     float ref = -INFINITY, l = 0.f;
-    for (int j = 0; j < steps[x]; ++j) {
-      if (!__all_sync(0xffffffffu, wait(&bar->s_full[x], j & 1))) return;
+    for (int j = 0; j < mine; ++j) {
+      if (!__all_sync(0xffffffffu, wait(&bar->s_full[x], (done + j) & 1))) return false;
       tc_fence_after();
       constexpr int kHeld = Gm::kTwice ? 64 : kApKeys;
       float s[kHeld];
@@ -445,7 +617,7 @@ struct ApBlock {
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kHeld - 4 + e]);
         return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       };
-      const bool one = short_[x] && j + 1 == steps[x];  // (the same for all of the tile)
+      const bool one = cut && j + 1 == mine;  // (the same for all of the tile)
       float top = take(0);
       if constexpr (Gm::kTwice) {
         if (!one) top = fmaxf(top, take(64));
@@ -457,7 +629,7 @@ struct ApBlock {
           const float f = now == ref ? 1.f : ref == -INFINITY ? 0.f : ex2((ref - now) * c);
           l *= f;
           // the products up to step j - 1 are in O
-          if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (j - 1) & 1))) return;
+          if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (done + j - 1) & 1))) return false;
           tc_fence_after();
 #pragma unroll 1  // (rare)
           for (int i = 0; i < D; i += 32) {
@@ -472,11 +644,12 @@ struct ApBlock {
         ref = now;
       }
       if ((j + 1) * kApKeys > T.nk) {  // the sequence's last, partial step: V behind it as zeros
-        if (!__all_sync(0xffffffffu, wait(&bar->v_full[j % Gm::kStages], (j / Gm::kStages) & 1))) return;
+        const uint32_t u = use + j;
+        if (!__all_sync(0xffffffffu, wait(&bar->v_full[u % Gm::kStages], (u / Gm::kStages) & 1))) return false;
         const int first = T.nk - j * kApKeys;
         for (int i = threadIdx.x & 127; i < (kApKeys - first) * Gm::kHalves * 8; i += 128) {
           const int r = first + i / (8 * Gm::kHalves), e = i % (8 * Gm::kHalves);
-          *reinterpret_cast<uint4*>(v_at(j % Gm::kStages) + (e / 8) * Gm::kBlock + r * 128 + (e % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v_at(u % Gm::kStages) + (e / 8) * Gm::kBlock + r * 128 + (e % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
       }
@@ -507,8 +680,8 @@ struct ApBlock {
     // the output rows (zeros where a row has seen nothing), through the tile's Q rows, which the
     // last score product has read, so that a row's bytes leave together
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (steps[x] > 0) {
-      if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (steps[x] - 1) & 1))) return;
+    if (mine > 0) {
+      if (!__all_sync(0xffffffffu, wait(&bar->o_full[x], (done + mine - 1) & 1))) return false;
       tc_fence_after();
     }
     // rolled loops: this runs once, and unrolled it would wait for its instructions
@@ -521,12 +694,13 @@ struct ApBlock {
       for (int e = 0; e < 64; e += 8) {
         uint4 v = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
                              pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-        if (steps[x] == 0) v = make_uint4(0u, 0u, 0u, 0u);  // O was never written
+        // O was never written; Q's rows behind the last token stay zeros
+        if (mine == 0 || !whole) v = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(at + (((e / 8) ^ (row & 7)) << 4)) = v;
       }
     }
     __syncwarp();
-    const long long mine = live ? ((static_cast<long long>(T.q0) + tok) * p.q_heads + head) * D : -1;
+    const long long out = live ? ((static_cast<long long>(T.q0) + tok) * p.q_heads + head) * D : -1;
     constexpr int kLanes = D / 8;  // of a row
 #pragma unroll 1
     for (int i = 0; i < kLanes; i += 4) {
@@ -535,7 +709,7 @@ struct ApBlock {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int from = (i + u) * (32 / kLanes) + lane / kLanes, r = (row & ~31) + from, e = lane % kLanes;
-        at[u] = __shfl_sync(0xffffffffu, mine, from);
+        at[u] = __shfl_sync(0xffffffffu, out, from);
         v[u] = *reinterpret_cast<const uint4*>(q_at(x) + (e / 8) * Gm::kBlock + r * 128 + (((e % 8) ^ (r & 7)) << 4));
       }
 #pragma unroll
@@ -543,12 +717,25 @@ struct ApBlock {
         if (at[u] >= 0) *reinterpret_cast<uint4*>(p.out + at[u] + 8 * (lane % kLanes)) = v[u];
     }
     tc_fence_before();
+    if (Waves) {
+      fence_proxy_async_smem();  // the next unit's Q comes behind these reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->q_free[x]);
+    }
+    return true;
   }
 };
 
-// Blocks over (unit, key/value head), heads fastest and a sequence's last queries, which see
-// the most keys, first.
-template <int D, int X>
+// A block per (unit, key/value head).  One that has started takes over the work of blocks that have
+// not (clusterlaunchcontrol), unit after unit: its setup and tensor memory, its search for a
+// sequence and the 2 us between one block's end and the next one's first product come once, or
+// under another unit's work, and the device still balances the load.  The loading warp finds the
+// units and hands them to the others through a queue of two.  With and without (us, 32 over 8
+// heads of 128): 64 prompts of 128 tokens 47.0 and 58.5, 16 of 512 65.2 and 73.7, 8 of 1024 88.6 and
+// 97.7, one of 8192 (power-limited) 440 both.  Where all blocks fit on the device at once there is
+// nothing to take over, and Waves = false leaves it out (one prompt of 512 tokens, heads of 64: 10.1
+// us, with it 10.4 to 10.9).
+template <int D, int X, bool Waves>
 __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks) attn_prompt_kernel(const __grid_constant__ ApParams p) {
   using Gm = ApGeom<D, X>;
   extern __shared__ uint8_t ap_smem[];
@@ -558,10 +745,11 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
   }
   uint8_t* base = ap_smem + ((1024u - (smem_u32(ap_smem) & 1023u)) & 1023u);
   ApBars* bar = reinterpret_cast<ApBars*>(base + Gm::kBars);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 32 * Gm::kLoadWarp) {
     for (int i = 0; i < X; ++i) {
       mbar_init(&bar->q_full[i], 1);
+      mbar_init(&bar->q_free[i], 4);
       mbar_init(&bar->s_full[i], 1);
       mbar_init(&bar->p_full[i][0], 4);
       mbar_init(&bar->p_full[i][1], 4);
@@ -573,6 +761,11 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
       mbar_init(&bar->v_full[i], 1);
       mbar_init(&bar->v_empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->work_full[i], 1);
+      mbar_init(&bar->work_empty[i], 1 + 4 * X);
+    }
+    mbar_init(&bar->answered, 1);
     mbar_init(&bar->drain, 1);
     bar->abort_flag = 0;
     mbar_init_fence();
@@ -583,19 +776,8 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
   fence_proxy_async_smem();
   grid_launch_dependents();
   grid_dependency_wait();
-  ApBlock<D, X> B{p, base, bar};
-  const bool work = ap_find(p, p.units - 1 - static_cast<int>(blockIdx.x / p.kv_heads), X * p.tile_tokens, B.T);
-  B.kvh = blockIdx.x % p.kv_heads;
-  bool some = false;
-#pragma unroll
-  for (int x = 0; x < X; ++x) {
-    const int t0 = B.T.first + x * p.tile_tokens, last = min(B.T.nq, t0 + p.tile_tokens) - 1;
-    const int keys = work && t0 < B.T.nq ? max(0, last + B.T.nk - B.T.nq + 1) : 0;
-    B.steps[x] = (keys + kApKeys - 1) / kApKeys;
-    B.short_[x] = keys > 0 && (keys - 1) % kApKeys < kApKeys / 2;
-    some |= keys > 0;
-  }
-  if (some && threadIdx.x == 32 * Gm::kLoadWarp) B.load_first();
+  ApBlock<D, X, Waves> B{p, base, bar};
+  if (warp == Gm::kLoadWarp) B.begin();
   if (warp == Gm::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar->tmem)), "r"(Gm::kTmem)
                  : "memory");
@@ -607,13 +789,11 @@ __global__ void __launch_bounds__(ApGeom<D, X>::kThreads, ApGeom<D, X>::kBlocks)
   const uint32_t tmem = bar->tmem;
   if (warp < 4 * X) {
     if constexpr (X == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    if (work) B.soften(warp >> 2, tmem);
+    B.soften(warp >> 2, tmem);
   } else {
     if constexpr (X == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (some) {
-      if (warp == Gm::kMmaWarp) B.multiply(tmem);
-      if (warp == Gm::kLoadWarp && lane == 0) B.load();
-    }
+    if (warp == Gm::kMmaWarp) B.multiply(tmem);
+    if (warp == Gm::kLoadWarp) B.load();
   }
   tc_fence_before();
   __syncthreads();

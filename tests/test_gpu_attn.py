@@ -441,6 +441,14 @@ def test_prompt(attn, H, KV, D, lq, more):
     _check_prompt(q, k, v, cq, ck, D ** -0.5, out)
 
 
+@pytest.mark.parametrize("H,KV,D,top,seqs", [(24, 8, 64, 260, 45), (16, 16, 128, 130, 40), (6, 6, 64, 600, 40), (40, 8, 128, 90, 70)])
+def test_prompt_more_work_than_blocks_at_once(attn, H, KV, D, top, seqs):
+    """Packed lengths of any kind, empty ones and queries without keys among them, several units to a block."""
+    rng = np.random.default_rng(H + top)
+    lq = [int(n) for n in rng.integers(0, top, seqs)]
+    test_prompt(attn, H, KV, D, lq, [int(n) for n in rng.integers(-top, top // 2, seqs)])
+
+
 def test_prompt_strides_and_other_sequences(attn):
     """Views of one fused buffer; NaN and infinities in the sequences around one."""
     rng = np.random.default_rng(9)
@@ -490,6 +498,24 @@ def test_prompt_large_scores(attn):
         out = torch.empty(300, 2, 128, dtype=torch.bfloat16, device="cuda")
         attn.fmoe_attn_prompt(cfg, q, k, v, _i32([0, 300]), _i32([0, 300]), out, scale)
         _check_prompt(q, k, v, [0, 300], [0, 300], scale, out)
+
+
+def test_prompt_two_streams_at_once(attn):
+    """Two calls side by side, each with more blocks than fit: both as when alone."""
+    rng = np.random.default_rng(21)
+    cfg = attn.fmoe_attn_config(16, 8, 128)
+    cu = _i32(np.concatenate([[0], np.cumsum(rng.integers(1, 200, 60))]))
+    rows = int(cu[-1])
+    jobs = [[_bf16(rng, rows, h, 128) for h in (16, 8, 8)] for _ in range(2)]
+    alone = [attn.fmoe_attn_prompt(cfg, *j, cu, cu, torch.empty_like(j[0]), 0.09) for j in jobs]
+    outs = [torch.empty_like(j[0]) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for j, out, stream in zip(jobs, outs, streams):
+            attn.fmoe_attn_prompt(cfg, *j, cu, cu, out, 0.09, stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(alone, outs))
 
 
 def test_prompt_stream_graph_and_repeat(attn):
