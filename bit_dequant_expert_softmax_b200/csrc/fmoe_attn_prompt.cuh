@@ -165,8 +165,8 @@ struct ApLine {
     seek(p, 0, 0, INT64_MAX, tile_tokens);
     total = __shfl_sync(0xffffffffu, upto, 31);
   }
-  // the unit at place `at` < total
-  __device__ __forceinline__ void find(const ApParams& p, long long at, int tile_tokens, ApTile& r) {
+  // the unit at place `at` < total (false: the offsets are no longer what they were)
+  __device__ __forceinline__ bool find(const ApParams& p, long long at, int tile_tokens, ApTile& r) {
     if (at < base || at >= __shfl_sync(0xffffffffu, upto, 31)) {
       if (at < base)
         seek(p, 0, 0, at, tile_tokens);
@@ -174,11 +174,13 @@ struct ApLine {
         seek(p, s0 + 32, __shfl_sync(0xffffffffu, upto, 31), at, tile_tokens);
     }
     const int who = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+    if (who < 0) return false;
     r.q0 = __shfl_sync(0xffffffffu, own.q0, who);
     r.nq = __shfl_sync(0xffffffffu, own.nq, who);
     r.k0 = __shfl_sync(0xffffffffu, own.k0, who);
     r.nk = __shfl_sync(0xffffffffu, own.nk, who);
     r.first = static_cast<int>(at - __shfl_sync(0xffffffffu, upto - mine, who)) * tile_tokens;
+    return true;
   }
 };
 
@@ -340,7 +342,6 @@ struct ApBlock {
   int kvh;
   int steps[X];    // key steps of the row tiles
   bool short_[X];  // the last of them sees no key of its second half
-
   int n;           // the longest of them
 
   __device__ __forceinline__ void plan() {
@@ -401,10 +402,8 @@ struct ApBlock {
   // unit `back` from the line's end, of head kvh
   __device__ __forceinline__ void find(int back) {
     const long long at = line.total - 1 - back;
-    has = at >= 0;
-    if (!has) return;
-    line.find(p, at, X * p.tile_tokens, T);
-    plan();
+    has = at >= 0 && line.find(p, at, X * p.tile_tokens, T);
+    if (has) plan();
   }
   // before the block meets: the first unit and its first loads
   __device__ __forceinline__ void begin() {
