@@ -15,6 +15,8 @@
  * device_error (every call): NULL, or a uint32_t in device memory into which the kernels
  * OR the FMOE_DEVERR_* bits below for indices that they found out of range.  Such an index
  * is never dereferenced: its row or its keys are left out, the rest of the call is done.
+ * FMOE_DEVERR_COPY_TIMEOUT says that a wait inside fmoe_attn_decode or fmoe_attn_prompt ran out
+ * (2 s): the call's outputs are then undefined.
  */
 #ifndef FMOE_ATTN_H
 #define FMOE_ATTN_H
